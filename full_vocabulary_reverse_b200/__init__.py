@@ -16,3 +16,4 @@ from .binding import (  # noqa: F401
     REDUCE_NONE, REDUCE_TOKEN_MEAN, REDUCE_SEQ_MEAN_NESTED,
     PAYLOAD_HIDDEN, PAYLOAD_LOGITS, PAYLOAD_LOGITS_PAIR,
 )
+from .optim import AdamW, grad_norm  # noqa: F401

@@ -43,6 +43,7 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
+_f64 = ctypes.c_double
 
 _SIGS = {
     "rkl_version": ([], ctypes.c_char_p),
@@ -83,6 +84,11 @@ _SIGS = {
                                  _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "rkl_backward_topk_logits": ([_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp,
                                   _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "rkl_adamw_state_size": ([_i32, _vp, _vp, _vp], _i32),
+    "rkl_adamw_step": ([_i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _f64, _vp, _f64,
+                        _f64, _f64, ctypes.c_uint32, _vp, _f64, _vp], _i32),
+    "rkl_grad_norm_workspace_size": ([_i32, ctypes.POINTER(_sz)], _i32),
+    "rkl_grad_norm": ([_i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "rkl_device_error": ([ctypes.POINTER(_i32)], _i32),
     "rkl_kernel_count": ([], _i32),
     "rkl_kernel_name": ([_i32], ctypes.c_char_p),

@@ -25,7 +25,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "librkl.so")
 LIB_DEBUG = os.path.join(HERE, "librkl_debug.so")
-SOURCES = ["api.cu", "tc_kernels.cu", "small_kernels.cu", "simt_kernels.cu", "topk_kernels.cu"]
+SOURCES = ["api.cu", "tc_kernels.cu", "small_kernels.cu", "simt_kernels.cu", "topk_kernels.cu",
+           "optim_kernels.cu"]
 HEADERS = ["kernels.h", "sm100.cuh", "bounds.cuh"]
 
 
@@ -49,7 +50,7 @@ def build(force=False, verbose=False, debug=False):
     if not force and not _stale(lib):
         return lib
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "--cudart", "static", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+           "--threads", "0", "--cudart", "static", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
            "-I", os.path.join(ROOT, "include"), "-o", lib + ".tmp"]
     if debug:
         cmd += ["-DRKL_DEBUG"]

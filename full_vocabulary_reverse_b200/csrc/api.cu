@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -59,7 +60,7 @@ static const char* const kKernelNames[K_COUNT] = {
     "scatter_loss", "reduce_loss",   "row_weights",  "dz_dual_tc",    "dz_single_tc", "grad_dw_dh_tc",
     "scatter_dh",   "fwd_simt_fp32", "dz_simt_fp32", "grad_simt_fp32", "pair_fwd",   "pair_bwd",
     "count_teachers", "build_slots", "topk_fwd", "topk_bwd", "zw_dual_tc", "dz_topk_tc", "topk_rowk",
-    "zw_single_tc", "dz_topk_single_tc"};
+    "zw_single_tc", "dz_topk_single_tc", "adamw", "adamw8", "norm_partial", "norm_final"};
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_COUNT) ? kKernelNames[id] : nullptr; }
 
@@ -319,6 +320,21 @@ static rkl_status check_ptr(const void* p, const char* name, bool required = tru
   if (p == nullptr) return required ? fail(RKL_ERR_NULL, "%s is NULL", name) : RKL_OK;
   if (!aligned16(p)) return fail(RKL_ERR_ALIGN, "%s is not 16-byte aligned", name);
   return RKL_OK;
+}
+
+// Element counts of the tensors of an optimizer step or a gradient norm.
+static rkl_status check_tensor_counts(int32_t n, const int64_t* numel) {
+  if (n < 0) return fail(RKL_ERR_SHAPE, "n = %d is negative", n);
+  if (n > 0 && numel == nullptr) return fail(RKL_ERR_NULL, "numel is NULL");
+  for (int32_t i = 0; i < n; ++i)
+    if (numel[i] < 0 || numel[i] >= (int64_t(1) << 37))
+      return fail(RKL_ERR_SHAPE, "tensor %d has %lld elements", i, (long long)numel[i]);
+  return RKL_OK;
+}
+
+// Whether 8 consecutive elements can move as one access a lane.
+static bool wide_access(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == RKL_BF16 ? 15 : 31)) == 0;
 }
 
 // The optional device row count: one int32, 4-byte aligned.
@@ -1106,18 +1122,202 @@ rkl_status rkl_backward_hidden_multi(const void* h_s, const void* h_t, const voi
 rkl_status rkl_device_error(int32_t* code) {
   if (code == nullptr) return fail(RKL_ERR_NULL, "code is NULL");
   RKL_CUDA(cudaDeviceSynchronize());
-  int v = 0, line_tc = 0, line_small = 0;
+  int v = 0, line_tc = 0, line_small = 0, line_optim = 0;
   RKL_CUDA(read_and_clear_device_error(&v));
   RKL_CUDA(read_and_clear_bounds_tc(&line_tc));
   RKL_CUDA(read_and_clear_bounds_small(&line_small));
-  if (line_tc || line_small) v |= ERR_BOUNDS;
+  RKL_CUDA(read_and_clear_bounds_optim(&line_optim));
+  if (line_tc || line_small || line_optim) v |= ERR_BOUNDS;
   *code = v;
-  if (line_tc || line_small)
+  if (line_tc || line_small || line_optim)
     return fail(RKL_ERR_DEVICE,
-                "a bounds check failed (tc_kernels.cu line %d, small_kernels.cu line %d; 0 = none); the access was "
-                "skipped and the outputs are invalid (bits 0x%x)",
-                line_tc, line_small, v);
+                "a bounds check failed (tc_kernels.cu line %d, small_kernels.cu line %d, optim_kernels.cu line %d; "
+                "0 = none); the access was skipped and the outputs are invalid (bits 0x%x)",
+                line_tc, line_small, line_optim, v);
   if (v != 0) return fail(RKL_ERR_DEVICE, "a kernel wait ran out (bits 0x%x); its outputs are invalid", v);
+  return RKL_OK;
+}
+
+// ====================================================================== optimizer step
+rkl_status rkl_adamw_state_size(int32_t n, const int64_t* numel, int64_t* at, int64_t* total) {
+  if (total == nullptr) return fail(RKL_ERR_NULL, "total is NULL");
+  RKL_TRY(check_tensor_counts(n, numel));
+  int64_t sum = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (at != nullptr) at[i] = sum;
+    sum += (numel[i] + kOptBlock - 1) / kOptBlock * kOptBlock;
+  }
+  *total = sum;
+  return RKL_OK;
+}
+
+rkl_status rkl_adamw_step(int32_t n, void* const* params, const void* const* grads, const int64_t* numel,
+                          const int32_t* param_dtype, const int32_t* grad_dtype, const float* weight_decay,
+                          int32_t state_bits, void* exp_avg, void* exp_avg_sq, float* exp_avg_scale,
+                          float* exp_avg_sq_scale, float* master, int32_t* control, double lr, const float* lr_dev,
+                          double beta1, double beta2, double eps, uint32_t seed, const float* norm, double max_norm,
+                          void* stream) {
+  RKL_NVTX_RANGE();
+  RKL_TRY(check_tensor_counts(n, numel));
+  if (n > 0 && (params == nullptr || grads == nullptr || param_dtype == nullptr || grad_dtype == nullptr ||
+                weight_decay == nullptr))
+    return fail(RKL_ERR_NULL, "params, grads, param_dtype, grad_dtype and weight_decay must be non-NULL");
+  if (state_bits != 32 && state_bits != 8) return fail(RKL_ERR_DTYPE, "state_bits = %d is neither 32 nor 8", state_bits);
+  if (control == nullptr) return fail(RKL_ERR_NULL, "control is NULL");
+  if (reinterpret_cast<uintptr_t>(control) & 7) return fail(RKL_ERR_ALIGN, "control is not 8-byte aligned");
+  if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1))
+    return fail(RKL_ERR_SHAPE, "betas (%g, %g) outside [0, 1)", beta1, beta2);
+  if (!(eps >= 0)) return fail(RKL_ERR_SHAPE, "eps = %g is negative", eps);
+  if (lr_dev == nullptr && !(lr >= 0)) return fail(RKL_ERR_SHAPE, "lr = %g is negative", lr);
+  if (norm != nullptr && !(max_norm > 0)) return fail(RKL_ERR_SHAPE, "max_norm = %g is not positive", max_norm);
+  for (const float* p : {lr_dev, norm})
+    if (reinterpret_cast<uintptr_t>(p) & 3) return fail(RKL_ERR_ALIGN, "lr_dev or norm is not 4-byte aligned");
+  int64_t total = 0;
+  RKL_TRY(rkl_adamw_state_size(n, numel, nullptr, &total));
+  if (total > 0) {
+    // the state is read and written 8 elements a lane
+    const struct { const void* p; const char* name; bool need; } state[] = {
+        {exp_avg, "exp_avg", true},
+        {exp_avg_sq, "exp_avg_sq", true},
+        {exp_avg_scale, "exp_avg_scale", state_bits == 8},
+        {exp_avg_sq_scale, "exp_avg_sq_scale", state_bits == 8},
+        {master, "master", false}};
+    for (const auto& x : state) {
+      if (x.need && x.p == nullptr) return fail(RKL_ERR_NULL, "%s is NULL", x.name);
+      if (reinterpret_cast<uintptr_t>(x.p) & 31) return fail(RKL_ERR_ALIGN, "%s is not 32-byte aligned", x.name);
+    }
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    if (param_dtype[i] != RKL_BF16 && param_dtype[i] != RKL_FP32)
+      return fail(RKL_ERR_DTYPE, "unknown dtype %d of parameter %d", param_dtype[i], i);
+    if (grad_dtype[i] != RKL_BF16 && grad_dtype[i] != RKL_FP32)
+      return fail(RKL_ERR_DTYPE, "unknown dtype %d of gradient %d", grad_dtype[i], i);
+    if (numel[i] == 0 || grads[i] == nullptr) continue;
+    if (params[i] == nullptr) return fail(RKL_ERR_NULL, "parameter %d is NULL", i);
+    if (reinterpret_cast<uintptr_t>(params[i]) & (param_dtype[i] == RKL_BF16 ? 1 : 3))
+      return fail(RKL_ERR_ALIGN, "parameter %d is not aligned to its elements", i);
+    if (reinterpret_cast<uintptr_t>(grads[i]) & (grad_dtype[i] == RKL_BF16 ? 1 : 3))
+      return fail(RKL_ERR_ALIGN, "gradient %d is not aligned to its elements", i);
+  }
+  int sms = 0;
+  RKL_TRY(device_setup(&sms));
+  AdamwArgs a;
+  a.total = total;
+  a.m = exp_avg;
+  a.v = exp_avg_sq;
+  a.m_scale = exp_avg_scale;
+  a.v_scale = exp_avg_sq_scale;
+  a.master = master;
+  a.control = control;
+  a.norm = norm;
+  a.lr_dev = lr_dev;
+  a.lr = static_cast<float>(lr);
+  a.beta1 = static_cast<float>(beta1);
+  a.beta2 = static_cast<float>(beta2);
+  a.omb1 = static_cast<float>(1 - beta1);
+  a.omb2 = static_cast<float>(1 - beta2);
+  a.log_beta1 = static_cast<float>(log(beta1));  // -inf for 0: 1 - b^t = 1
+  a.log_beta2 = static_cast<float>(log(beta2));
+  a.eps = static_cast<float>(eps);
+  a.max_norm = static_cast<float>(max_norm);
+  a.seed = seed;
+  a.n = 0;
+  a.blocks = 0;
+  int64_t at = 0;
+  for (int32_t i = 0; i <= n; ++i) {
+    const int64_t blocks = i < n ? (numel[i] + kOptBlock - 1) / kOptBlock : 0;
+    const bool taken = i < n && numel[i] > 0 && grads[i] != nullptr;
+    if (i == n || (taken && (a.n == kOptTensors || a.blocks + blocks > INT32_MAX / 2))) {
+      // (a step with nothing to update still counts)
+      a.advance = i == n;
+      const int64_t need = (a.blocks + kOptWarps - 1) / kOptWarps;
+      const int64_t most = int64_t(sms) * kOptGridPerSm;
+      RKL_CUDA(launch_adamw(state_bits, a, static_cast<int>(need < 1 ? 1 : (need < most ? need : most)),
+                            static_cast<cudaStream_t>(stream)));
+      a.n = 0;
+      a.blocks = 0;
+    }
+    if (taken) {
+      AdamwTensor& x = a.t[a.n];
+      x.param = params[i];
+      x.grad = grads[i];
+      x.n = numel[i];
+      x.at = at;
+      x.decay = weight_decay[i];
+      x.flags = (param_dtype[i] == RKL_BF16 ? OPT_PARAM_BF16 : 0u) | (grad_dtype[i] == RKL_BF16 ? OPT_GRAD_BF16 : 0u) |
+                (wide_access(params[i], param_dtype[i]) ? OPT_WIDE_PARAM : 0u) |
+                (wide_access(grads[i], grad_dtype[i]) ? OPT_WIDE_GRAD : 0u);
+      a.first[a.n++] = a.blocks;
+      a.blocks += static_cast<int>(blocks);
+    }
+    at += blocks * kOptBlock;
+  }
+  return RKL_OK;
+}
+
+rkl_status rkl_grad_norm_workspace_size(int32_t n, size_t* bytes) {
+  if (bytes == nullptr) return fail(RKL_ERR_NULL, "bytes is NULL");
+  if (n < 0) return fail(RKL_ERR_SHAPE, "n = %d is negative", n);
+  const size_t launches = n <= kOptTensors ? 1 : (n + kOptTensors - 1) / kOptTensors;
+  *bytes = launches * kNormMaxGrid * sizeof(double);
+  return RKL_OK;
+}
+
+rkl_status rkl_grad_norm(int32_t n, const void* const* grads, const int64_t* numel, const int32_t* grad_dtype,
+                         float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  RKL_NVTX_RANGE();
+  RKL_TRY(check_tensor_counts(n, numel));
+  if (n > 0 && (grads == nullptr || grad_dtype == nullptr))
+    return fail(RKL_ERR_NULL, "grads and grad_dtype must be non-NULL");
+  if (norm == nullptr) return fail(RKL_ERR_NULL, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) & 3) return fail(RKL_ERR_ALIGN, "norm is not 4-byte aligned");
+  for (int32_t i = 0; i < n; ++i) {
+    if (grad_dtype[i] != RKL_BF16 && grad_dtype[i] != RKL_FP32)
+      return fail(RKL_ERR_DTYPE, "unknown dtype %d of gradient %d", grad_dtype[i], i);
+    if (reinterpret_cast<uintptr_t>(grads[i]) & (grad_dtype[i] == RKL_BF16 ? 1 : 3))
+      return fail(RKL_ERR_ALIGN, "gradient %d is not aligned to its elements", i);
+    if ((numel[i] + kNormChunk - 1) / kNormChunk > INT32_MAX / 2)
+      return fail(RKL_ERR_SHAPE, "gradient %d has too many elements", i);
+  }
+  size_t need_ws = 0;
+  RKL_TRY(rkl_grad_norm_workspace_size(n, &need_ws));
+  if (workspace == nullptr || workspace_bytes < need_ws)
+    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", need_ws);
+  RKL_TRY(check_ptr(workspace, "workspace"));
+  int sms = 0;
+  RKL_TRY(device_setup(&sms));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormArgs a;
+  a.n = 0;
+  int64_t chunks = 0;
+  int partials = 0;
+  for (int32_t i = 0; i <= n; ++i) {
+    const int64_t more = i < n ? (numel[i] + kNormChunk - 1) / kNormChunk : 0;
+    const bool taken = i < n && numel[i] > 0 && grads[i] != nullptr;
+    // a full table, or (a launch's chunks are counted in 32 bits) too many elements, begins another launch
+    if (a.n > 0 && (i == n || (taken && (a.n == kOptTensors || chunks + more > INT32_MAX / 2)))) {
+      a.chunks = static_cast<int>(chunks);
+      const int64_t need = (chunks + kOptWarps - 1) / kOptWarps;
+      const int most = sms * 8 < kNormMaxGrid ? sms * 8 : kNormMaxGrid;
+      const int grid = static_cast<int>(need < most ? need : most);
+      if ((partials + grid) * sizeof(double) > workspace_bytes)
+        return fail(RKL_ERR_SHAPE, "the gradients have too many elements for %d tensors", n);
+      a.partial = static_cast<double*>(workspace) + partials;
+      RKL_CUDA(launch_norm_partial(a, grid, s));
+      partials += grid;
+      a.n = 0;
+      chunks = 0;
+    }
+    if (taken) {
+      a.t[a.n].grad = grads[i];
+      a.t[a.n].n = numel[i];
+      a.t[a.n].flags = (grad_dtype[i] == RKL_BF16 ? OPT_GRAD_BF16 : 0u) |
+                       (wide_access(grads[i], grad_dtype[i]) ? OPT_WIDE_GRAD : 0u);
+      a.first[a.n++] = static_cast<int>(chunks);
+      chunks += more;
+    }
+  }
+  RKL_CUDA(launch_norm_final(static_cast<const double*>(workspace), partials, norm, s));
   return RKL_OK;
 }
 

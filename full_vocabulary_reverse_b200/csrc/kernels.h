@@ -38,6 +38,10 @@ enum KernelId : int {
   K_TOPK_ROWK,        // top-k, hidden payload: per-row constants of the dz pass
   K_ZW_SINGLE_TC,     // top-k, logits payload: z_s of a row block by tcgen05, shipped z_t copied beside it
   K_DZ_TOPK_SINGLE_TC,  // top-k, logits payload: recompute z_s + top-k dz chunk
+  K_ADAMW,            // AdamW step, 32-bit states
+  K_ADAMW8,           // AdamW step, 8-bit states
+  K_NORM_PARTIAL,     // gradient norm: partial sums of squares
+  K_NORM_FINAL,       // gradient norm: join
   K_COUNT
 };
 
@@ -158,6 +162,7 @@ cudaError_t read_and_clear_device_error(int* code);
 // since the last read (0: none), cleared by the read.
 cudaError_t read_and_clear_bounds_tc(int* line);
 cudaError_t read_and_clear_bounds_small(int* line);
+cudaError_t read_and_clear_bounds_optim(int* line);
 
 // ---------------------------------------------------------------- small kernels
 cudaError_t launch_compact(const uint8_t* mask, long long T, int32_t* row_idx, int32_t* n_dev, cudaStream_t s);
@@ -253,5 +258,56 @@ cudaError_t launch_simt_fused(bool dz, const SimtArgs& a, dim3 grid, cudaStream_
 cudaError_t launch_simt_gemm(const float* A, long long sam, long long sak, const float* B, long long sbk,
                              long long sbn, float* C, long long ldc, int M, int Nc, int K, int accumulate,
                              const int32_t* n_dev, int live_dim, cudaStream_t s);
+
+// ---------------------------------------------------------------- optimizer step
+constexpr int kOptBlock = 256;     // elements of a state block (one scale of the 8-bit form, one warp's work)
+constexpr int kOptWarps = 8;       // warps of a block of the optimizer kernels
+constexpr int kOptGridPerSm = 8;   // blocks per SM of the optimizer kernels' largest grid
+constexpr int kNormChunk = 1024;   // elements a warp of the norm kernel takes at a time
+constexpr int kOptTensors = 400;   // tensors of one launch (their table travels in the kernel's parameters)
+constexpr int kNormMaxGrid = 1184;  // blocks (partial sums) of one norm launch: 8 on each of 148 SMs
+enum : uint32_t {
+  OPT_PARAM_BF16 = 1,
+  OPT_GRAD_BF16 = 2,
+  OPT_WIDE_PARAM = 4,  // aligned for the 8-element accesses
+  OPT_WIDE_GRAD = 8,
+};
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  long long n, at;     // elements; first element in the state (a multiple of kOptBlock)
+  float decay;
+  uint32_t flags;
+};
+struct AdamwArgs {
+  AdamwTensor t[kOptTensors];
+  int first[kOptTensors];  // first block of each tensor in this launch
+  int n, blocks;           // tensors and blocks of this launch
+  long long total;         // elements of the state
+  void *m, *v;             // fp32 or e4m3
+  float *m_scale, *v_scale;
+  float* master;           // fp32 copies of the parameters (nullable)
+  int32_t* control;        // [steps done, ticket]
+  const float* norm;       // global gradient norm (nullable)
+  const float* lr_dev;     // learning rate on the device (nullable: lr)
+  float lr, beta1, beta2, omb1, omb2, log_beta1, log_beta2, eps, max_norm;
+  uint32_t seed;
+  int advance;             // the step's last launch: counts the step
+};
+cudaError_t launch_adamw(int bits, const AdamwArgs& a, int grid, cudaStream_t s);
+
+struct NormTensor {
+  const void* grad;
+  long long n;
+  uint32_t flags;
+};
+struct NormArgs {
+  NormTensor t[kOptTensors];
+  int first[kOptTensors];
+  int n, chunks;
+  double* partial;  // [grid]
+};
+cudaError_t launch_norm_partial(const NormArgs& a, int grid, cudaStream_t s);
+cudaError_t launch_norm_final(const double* partial, int n, float* norm, cudaStream_t s);
 
 }  // namespace rkl

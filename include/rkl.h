@@ -420,6 +420,63 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
                                       float* loss_tok, float* loss, float* saved,
                                       void* stream);
 
+/* ------------------------------------------------------------------------
+ * The optimizer step behind the loss's backward.
+ *
+ * AdamW with decoupled weight decay over n tensors at once.  For every element,
+ * with t = steps + 1 and c = min(1, max_norm / *norm) (1 without norm), all in
+ * fp32:
+ *
+ *     g = c grad
+ *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * The moments of all tensors are two flat arrays; rkl_adamw_state_size gives
+ * the first element at[i] of each tensor (a multiple of 256) and the arrays'
+ * length.  Elements between a tensor's end and the next tensor's start belong
+ * to the first one's last block; they must be zero at the beginning and stay so.
+ *   state_bits = 32: exp_avg and exp_avg_sq are fp32 [total]; no scales.
+ *   state_bits = 8:  they are e4m3 codes [total] and fp32 scales [total / 256];
+ *     a value is code x scale of its block of 256, scale = largest magnitude /
+ *     448.  A block no larger than 2^-100 is held as zeros.  exp_avg is rounded
+ *     to the nearest code (ties to even).  exp_avg_sq is rounded stochastically:
+ *     up when rest + r / 2^20 >= 1, and never from a positive value to 0, with
+ *     the 20-bit number r = mix(e ^ mix(key + (e >> 32))) >> 12 of element e of
+ *     the state, key = mix(t x 0x9E3779B1 + seed), all in 32 bits and mix the
+ *     final mix of MurmurHash3.  Equal calls give equal bits.
+ * master (fp32 [total], nullable): the parameters themselves in the state's
+ * layout; params then receive the rounded copies and are not read.
+ * control: int32 [2], 8-byte aligned, {steps done, 0} between steps.  The step
+ * counts itself on the device, so that a captured step can be replayed.
+ *
+ * params, grads, numel, param_dtype, grad_dtype and weight_decay are HOST
+ * arrays of n entries (the tensors themselves are on the device, contiguous,
+ * aligned to their elements).  A NULL grads[i] leaves tensor i and its state as
+ * they are.  No two tensors may overlap; gradients are only read.
+ * lr_dev (device, nullable) replaces lr.  norm (device, nullable): the global
+ * gradient norm.  If it is infinite or NaN the step changes nothing, not the
+ * step count either.  Calls on one state must be ordered by the caller. */
+rkl_status rkl_adamw_state_size(int32_t n, const int64_t* numel,
+                                int64_t* at /* host out [n], nullable */,
+                                int64_t* total /* host out */);
+rkl_status rkl_adamw_step(int32_t n, void* const* params, const void* const* grads,
+                          const int64_t* numel, const int32_t* param_dtype,
+                          const int32_t* grad_dtype, const float* weight_decay,
+                          int32_t state_bits, void* exp_avg, void* exp_avg_sq,
+                          float* exp_avg_scale, float* exp_avg_sq_scale, float* master,
+                          int32_t* control, double lr, const float* lr_dev,
+                          double beta1, double beta2, double eps, uint32_t seed,
+                          const float* norm, double max_norm, void* stream);
+
+/* norm[0] = sqrt(sum over all elements of all gradients of grad^2), summed in
+ * 64 bits (fp32 within groups of 8 whose squares fp32 holds).  grads, numel and
+ * grad_dtype are HOST arrays of n entries; a NULL gradient counts as absent.
+ * Infinite or NaN exactly where a gradient is, or where the norm leaves fp32. */
+rkl_status rkl_grad_norm_workspace_size(int32_t n, size_t* bytes /* host out */);
+rkl_status rkl_grad_norm(int32_t n, const void* const* grads, const int64_t* numel,
+                         const int32_t* grad_dtype, float* norm /* device out [1] */,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises the current device, then reports and clears the library's
  * device error word: *code = 0 if no kernel's bounded wait ran out since the
  * last call, else a nonzero bit set naming the wait (the kernel returned
