@@ -17,3 +17,4 @@ from .binding import (  # noqa: F401
     PAYLOAD_HIDDEN, PAYLOAD_LOGITS, PAYLOAD_LOGITS_PAIR,
 )
 from .optim import AdamW, grad_norm  # noqa: F401
+from .ffn import ffn_forward, ffn_backward, gated_ffn, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU  # noqa: F401

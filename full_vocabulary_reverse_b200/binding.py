@@ -84,6 +84,10 @@ _SIGS = {
                                  _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "rkl_backward_topk_logits": ([_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp,
                                   _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "rkl_ffn_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_sz)], _i32),
+    "rkl_ffn_forward": ([_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _i32),
+    "rkl_ffn_backward": ([_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                          _sz, _vp], _i32),
     "rkl_adamw_state_size": ([_i32, _vp, _vp, _vp], _i32),
     "rkl_adamw_step": ([_i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _f64, _vp, _f64,
                         _f64, _f64, ctypes.c_uint32, _vp, _f64, _vp], _i32),

@@ -19,6 +19,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "rkl.h"
+#include "ffn_act.cuh"
 #include "kernels.h"
 
 namespace rkl {
@@ -60,7 +61,8 @@ static const char* const kKernelNames[K_COUNT] = {
     "scatter_loss", "reduce_loss",   "row_weights",  "dz_dual_tc",    "dz_single_tc", "grad_dw_dh_tc",
     "scatter_dh",   "fwd_simt_fp32", "dz_simt_fp32", "grad_simt_fp32", "pair_fwd",   "pair_bwd",
     "count_teachers", "build_slots", "topk_fwd", "topk_bwd", "zw_dual_tc", "dz_topk_tc", "topk_rowk",
-    "zw_single_tc", "dz_topk_single_tc", "adamw", "adamw8", "norm_partial", "norm_final"};
+    "zw_single_tc", "dz_topk_single_tc", "adamw", "adamw8", "norm_partial", "norm_final",
+    "ffn_up_simt", "ffn_dgate_simt", "ffn_gemm_simt"};
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_COUNT) ? kKernelNames[id] : nullptr; }
 
@@ -1318,6 +1320,122 @@ rkl_status rkl_grad_norm(int32_t n, const void* const* grads, const int64_t* num
     }
   }
   RKL_CUDA(launch_norm_final(static_cast<const double*>(workspace), partials, norm, s));
+  return RKL_OK;
+}
+
+// ====================================================================== gated feed-forward block
+static rkl_status check_ffn(rkl_dtype dtype, int activation, int64_t T, int64_t H, int64_t F, int64_t O) {
+  if (dtype != RKL_BF16 && dtype != RKL_FP32) return fail(RKL_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+  if (activation < ACT_SILU || activation > ACT_RELU) return fail(RKL_ERR_DTYPE, "unknown activation %d", activation);
+  if (T < 0 || H < 1 || F < 1 || O < 1) return fail(RKL_ERR_SHAPE, "T must be >= 0 and H, F, O >= 1");
+  if (T >= (int64_t(1) << 30) || H > (1 << 20) || F > (1 << 20) || O > (1 << 20))
+    return fail(RKL_ERR_SHAPE, "T = %lld, H = %lld, F = %lld, O = %lld: too large", (long long)T, (long long)H,
+                (long long)F, (long long)O);
+  return RKL_OK;
+}
+
+// The gated block's tensors are aligned to their elements.
+static rkl_status check_ffn_ptr(const void* p, const char* name, rkl_dtype dtype, bool required = true) {
+  if (p == nullptr) return required ? fail(RKL_ERR_NULL, "%s is NULL", name) : RKL_OK;
+  if (reinterpret_cast<uintptr_t>(p) & (dtype == RKL_BF16 ? 1 : 3))
+    return fail(RKL_ERR_ALIGN, "%s is not aligned to its elements", name);
+  return RKL_OK;
+}
+
+static size_t ffn_workspace(rkl_dtype dtype, int64_t T, int64_t F, bool backward) {
+  const size_t plane = align256(size_t(T) * F * (dtype == RKL_BF16 ? 2 : 4));
+  return (backward ? 3 : 1) * plane + 256;
+}
+
+rkl_status rkl_ffn_workspace_size(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, int32_t backward,
+                                  size_t* bytes) {
+  if (bytes == nullptr) return fail(RKL_ERR_NULL, "bytes is NULL");
+  RKL_TRY(check_ffn(dtype, ACT_SILU, T, H, F, O));
+  *bytes = ffn_workspace(dtype, T, F, backward != 0);
+  return RKL_OK;
+}
+
+rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up, const void* W_down, rkl_dtype dtype,
+                           int32_t activation, int64_t T, int64_t H, int64_t F, int64_t O, void* y, float* saved,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  RKL_NVTX_RANGE();
+  RKL_TRY(check_ffn(dtype, activation, T, H, F, O));
+  RKL_TRY(check_ffn_ptr(W_gate, "W_gate", dtype));
+  RKL_TRY(check_ffn_ptr(W_up, "W_up", dtype));
+  RKL_TRY(check_ffn_ptr(W_down, "W_down", dtype));
+  if (T == 0) return RKL_OK;
+  RKL_TRY(check_ffn_ptr(x, "x", dtype));
+  RKL_TRY(check_ffn_ptr(y, "y", dtype));
+  RKL_TRY(check_ptr(saved, "saved", false));
+  const size_t need = ffn_workspace(dtype, T, F, false);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", need);
+  RKL_TRY(check_ptr(workspace, "workspace"));
+  int sms = 0;
+  RKL_TRY(device_setup(&sms));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == RKL_BF16;
+  FfnSimtArgs a = {};
+  a.n = 1;
+  a.act = activation;
+  a.saved = saved;
+  // a = act(x Wg^T) (x Wu^T)
+  a.p[0] = {{x, nullptr}, {W_gate, W_up}, workspace, T, F, H, H, 1, 1, H, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_UP, bf16, a, sms, s));
+  // y = a Wd^T
+  a.p[0] = {{workspace, nullptr}, {W_down, nullptr}, y, T, O, F, F, 1, 1, F, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_GEMM, bf16, a, sms, s));
+  return RKL_OK;
+}
+
+rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up, const void* W_down, rkl_dtype dtype,
+                            int32_t activation, int64_t T, int64_t H, int64_t F, int64_t O, const void* dy,
+                            const float* saved, void* dx, void* dW_gate, void* dW_up, void* dW_down, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  RKL_NVTX_RANGE();
+  RKL_TRY(check_ffn(dtype, activation, T, H, F, O));
+  RKL_TRY(check_ffn_ptr(W_gate, "W_gate", dtype));
+  RKL_TRY(check_ffn_ptr(W_up, "W_up", dtype));
+  RKL_TRY(check_ffn_ptr(W_down, "W_down", dtype));
+  RKL_TRY(check_ffn_ptr(dx, "dx", dtype, false));
+  RKL_TRY(check_ffn_ptr(dW_gate, "dW_gate", dtype, false));
+  RKL_TRY(check_ffn_ptr(dW_up, "dW_up", dtype, false));
+  RKL_TRY(check_ffn_ptr(dW_down, "dW_down", dtype, false));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == RKL_BF16;
+  const size_t es = bf16 ? 2 : 4;
+  if (T == 0) {  // no rows: the weights' gradients are zero
+    if (dW_gate) RKL_CUDA(cudaMemsetAsync(dW_gate, 0, size_t(F) * H * es, s));
+    if (dW_up) RKL_CUDA(cudaMemsetAsync(dW_up, 0, size_t(F) * H * es, s));
+    if (dW_down) RKL_CUDA(cudaMemsetAsync(dW_down, 0, size_t(O) * F * es, s));
+    return RKL_OK;
+  }
+  RKL_TRY(check_ffn_ptr(x, "x", dtype));
+  RKL_TRY(check_ffn_ptr(dy, "dy", dtype));
+  RKL_TRY(check_ptr(saved, "saved"));
+  const size_t need = ffn_workspace(dtype, T, F, true);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", need);
+  RKL_TRY(check_ptr(workspace, "workspace"));
+  if (!dx && !dW_gate && !dW_up && !dW_down) return RKL_OK;
+  int sms = 0;
+  RKL_TRY(device_setup(&sms));
+  FfnSimtArgs a = {};
+  a.act = activation;
+  a.saved = const_cast<float*>(saved);
+  uint8_t* act = static_cast<uint8_t*>(workspace);  // a, dg and du, [T, F] each
+  const uint8_t* dg = act + size_t(T) * F * es;
+  const uint8_t* du = dg + size_t(T) * F * es;
+  // da = dy Wd -> a, dg, du
+  a.n = 1;
+  a.p[0] = {{dy, nullptr}, {W_down, nullptr}, act, T, F, O, O, 1, F, 1, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_DGATE, bf16, a, sms, s));
+  a.n = 0;
+  if (dx) a.p[a.n++] = {{dg, du}, {W_gate, W_up}, dx, T, H, F, F, 1, H, 1, 2, 0};
+  if (dW_gate) a.p[a.n++] = {{dg, nullptr}, {x, nullptr}, dW_gate, F, H, T, 1, F, H, 1, 1, 0};
+  if (dW_up) a.p[a.n++] = {{du, nullptr}, {x, nullptr}, dW_up, F, H, T, 1, F, H, 1, 1, 0};
+  if (dW_down) a.p[a.n++] = {{dy, nullptr}, {act, nullptr}, dW_down, O, F, T, 1, O, F, 1, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_GEMM, bf16, a, sms, s));
   return RKL_OK;
 }
 

@@ -42,6 +42,9 @@ enum KernelId : int {
   K_ADAMW8,           // AdamW step, 8-bit states
   K_NORM_PARTIAL,     // gradient norm: partial sums of squares
   K_NORM_FINAL,       // gradient norm: join
+  K_FFN_UP_SIMT,      // gated block on the CUDA cores: both projections, activation, product
+  K_FFN_DGATE_SIMT,   // gated block on the CUDA cores: da and the gradients of g and u
+  K_FFN_GEMM_SIMT,    // gated block on the CUDA cores: down projection, dx and weight gradients
   K_COUNT
 };
 
@@ -309,5 +312,24 @@ struct NormArgs {
 };
 cudaError_t launch_norm_partial(const NormArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_norm_final(const double* partial, int n, float* norm, cudaStream_t s);
+
+// ---------------------------------------------------------------- gated feed-forward block
+enum : int { FFN_UP = 0, FFN_DGATE = 1, FFN_GEMM = 2 };  // what a product's results go through
+// C(m, n) = sum over segments and k of A_s(m, k) B_s(k, n), row-major C [M, N].
+// FFN_UP: b[0] and b[1] are the gate and up weights, c = act(g) u.
+// FFN_DGATE: c receives a, dg and du, [3][M, N].
+struct FfnProduct {
+  const void *a[2], *b[2];
+  void* c;
+  long long M, N, K, sam, sak, sbk, sbn;  // strides in elements; sak or sam is 1, sbk or sbn is 1
+  int segments, first_tile;
+};
+constexpr int kFfnProducts = 4;
+struct FfnSimtArgs {
+  FfnProduct p[kFfnProducts];
+  float* saved;  // g and u, fp32 [2][M, N] (FFN_UP: nullable)
+  int n, act;
+};
+cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s);
 
 }  // namespace rkl

@@ -421,6 +421,49 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
                                       void* stream);
 
 /* ------------------------------------------------------------------------
+ * The gated feed-forward block in front of the head (the student's last block,
+ * an adapter or a draft head that trains with it):
+ *
+ *     g = x W_gate^T,  u = x W_up^T,  a = act(g) u,  y = a W_down^T
+ *
+ * x [T, H], W_gate and W_up [F, H], W_down [O, F], y [T, O]; all of one dtype,
+ * contiguous, aligned to their elements.  Any sizes: bf16 on 16-byte rows (H, F,
+ * O multiples of 8, 16-byte aligned tensors) runs on the tensor cores, the rest
+ * on the CUDA cores.  T = 0 is allowed (x, y, dy, dx and saved may be NULL).
+ *
+ * Products accumulate in fp32; g, u, act and its derivative are fp32.  a, and
+ * in the backward pass a, dg and du, are rounded once to dtype as operands of
+ * the next product.
+ *
+ * saved: fp32 [2][T, F], g and u for the backward pass (NULL in the forward pass
+ * alone: not stored).  The backward pass:
+ *
+ *     da = dy W_down,  dg = da u act'(g),  du = da act(g)
+ *     dx = dg W_gate + du W_up,  dW_gate = dg^T x,  dW_up = du^T x,
+ *     dW_down = dy^T a
+ *
+ * Each of its outputs (of dtype) may be NULL: it is left out.  relu'(0) = 0.
+ * The workspace (16-byte aligned) is free again when the call's work is done. */
+typedef enum rkl_activation {
+  RKL_ACT_SILU = 0,      /* g / (1 + e^-g) */
+  RKL_ACT_GELU = 1,      /* g Phi(g) */
+  RKL_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+  RKL_ACT_RELU = 3
+} rkl_activation;
+
+rkl_status rkl_ffn_workspace_size(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O,
+                                  int32_t backward, size_t* bytes /* host out */);
+rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up,
+                           const void* W_down, rkl_dtype dtype, int32_t activation,
+                           int64_t T, int64_t H, int64_t F, int64_t O, void* y, float* saved,
+                           void* workspace, size_t workspace_bytes, void* stream);
+rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
+                            const void* W_down, rkl_dtype dtype, int32_t activation,
+                            int64_t T, int64_t H, int64_t F, int64_t O, const void* dy,
+                            const float* saved, void* dx, void* dW_gate, void* dW_up,
+                            void* dW_down, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * The optimizer step behind the loss's backward.
  *
  * AdamW with decoupled weight decay over n tensors at once.  For every element,
