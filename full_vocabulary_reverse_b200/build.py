@@ -26,7 +26,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "librkl.so")
 LIB_DEBUG = os.path.join(HERE, "librkl_debug.so")
 SOURCES = ["api.cu", "tc_kernels.cu", "small_kernels.cu", "simt_kernels.cu", "topk_kernels.cu",
-           "optim_kernels.cu", "ffn_simt_kernels.cu"]
+           "optim_kernels.cu", "ffn_simt_kernels.cu",
+           "ffn_tc_kernels.cu"]
 HEADERS = ["kernels.h", "sm100.cuh", "bounds.cuh", "ffn_act.cuh"]
 
 

@@ -62,7 +62,8 @@ static const char* const kKernelNames[K_COUNT] = {
     "scatter_dh",   "fwd_simt_fp32", "dz_simt_fp32", "grad_simt_fp32", "pair_fwd",   "pair_bwd",
     "count_teachers", "build_slots", "topk_fwd", "topk_bwd", "zw_dual_tc", "dz_topk_tc", "topk_rowk",
     "zw_single_tc", "dz_topk_single_tc", "adamw", "adamw8", "norm_partial", "norm_final",
-    "ffn_up_simt", "ffn_dgate_simt", "ffn_gemm_simt"};
+    "ffn_up_simt", "ffn_dgate_simt", "ffn_gemm_simt", "ffn_up_tc", "ffn_dgate_tc", "ffn_gemm_tc", "ffn_skinny_tc",
+    "ffn_join"};
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_COUNT) ? kKernelNames[id] : nullptr; }
 
@@ -108,6 +109,9 @@ static rkl_status device_setup(int* sms) {
   int dev = 0;
   RKL_CUDA(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(RKL_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  // A thread that has made no runtime call yet (autograd's backward thread)
+  // has no current context, which encoding a tensor map needs.
+  RKL_CUDA(cudaSetDevice(dev));
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DevState& d = g_devs[dev];
   if (!d.ready) {
@@ -119,6 +123,7 @@ static rkl_status device_setup(int* sms) {
                   minor);
     RKL_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
     RKL_CUDA(tc_setup(dev));
+    RKL_CUDA(ffn_tc_setup());
     d.ready = true;
   }
   *sms = d.sms;
@@ -1124,18 +1129,21 @@ rkl_status rkl_backward_hidden_multi(const void* h_s, const void* h_t, const voi
 rkl_status rkl_device_error(int32_t* code) {
   if (code == nullptr) return fail(RKL_ERR_NULL, "code is NULL");
   RKL_CUDA(cudaDeviceSynchronize());
-  int v = 0, line_tc = 0, line_small = 0, line_optim = 0;
+  int v = 0, waits = 0, line_tc = 0, line_small = 0, line_optim = 0, line_ffn = 0;
   RKL_CUDA(read_and_clear_device_error(&v));
   RKL_CUDA(read_and_clear_bounds_tc(&line_tc));
   RKL_CUDA(read_and_clear_bounds_small(&line_small));
   RKL_CUDA(read_and_clear_bounds_optim(&line_optim));
-  if (line_tc || line_small || line_optim) v |= ERR_BOUNDS;
+  RKL_CUDA(read_and_clear_bounds_ffn(&line_ffn));
+  RKL_CUDA(read_and_clear_ffn_error(&waits));
+  v |= waits;
+  if (line_tc || line_small || line_optim || line_ffn) v |= ERR_BOUNDS;
   *code = v;
-  if (line_tc || line_small || line_optim)
+  if (line_tc || line_small || line_optim || line_ffn)
     return fail(RKL_ERR_DEVICE,
-                "a bounds check failed (tc_kernels.cu line %d, small_kernels.cu line %d, optim_kernels.cu line %d; "
-                "0 = none); the access was skipped and the outputs are invalid (bits 0x%x)",
-                line_tc, line_small, line_optim, v);
+                "a bounds check failed (tc_kernels.cu line %d, small_kernels.cu line %d, optim_kernels.cu line %d, "
+                "ffn_tc_kernels.cu line %d; 0 = none); the access was skipped and the outputs are invalid (bits 0x%x)",
+                line_tc, line_small, line_optim, line_ffn, v);
   if (v != 0) return fail(RKL_ERR_DEVICE, "a kernel wait ran out (bits 0x%x); its outputs are invalid", v);
   return RKL_OK;
 }
@@ -1342,16 +1350,240 @@ static rkl_status check_ffn_ptr(const void* p, const char* name, rkl_dtype dtype
   return RKL_OK;
 }
 
-static size_t ffn_workspace(rkl_dtype dtype, int64_t T, int64_t F, bool backward) {
-  const size_t plane = align256(size_t(T) * F * (dtype == RKL_BF16 ? 2 : 4));
-  return (backward ? 3 : 1) * plane + 256;
+// ---- plan of the gated block: sizes alone decide the layout, so that the
+// workspace that is asked for fits whichever path the addresses allow.
+constexpr int kPlanSms = 148;
+
+// ffn_skinny_kernel's share: `per` steps a CTA (4 at least: a part is written
+// and read again), and the most parts a tile has.
+struct SkinnyPlan {
+  int tiles = 0, tiles_first = 0, steps = 0, grid = 0, parts = 0, pitch = 0;
+  long long per = 0;
+};
+
+static SkinnyPlan skinny_plan(int64_t rows_first, int64_t rows_second, int64_t K) {
+  SkinnyPlan p;
+  p.tiles_first = static_cast<int>((rows_first + 127) / 128);
+  p.tiles = p.tiles_first + static_cast<int>((rows_second + 127) / 128);
+  p.steps = static_cast<int>((K + kBK - 1) / kBK);
+  const long long all = static_cast<long long>(p.tiles) * p.steps;
+  p.per = (all + kPlanSms - 1) / kPlanSms;
+  if (p.per < 4) p.per = 4;
+  p.grid = static_cast<int>((all + p.per - 1) / p.per);
+  for (long long t = 0; t < p.tiles; ++t) {
+    const int n = static_cast<int>(((t + 1) * p.steps - 1) / p.per - t * p.steps / p.per) + 1;
+    if (n > p.parts) p.parts = n;
+  }
+  p.pitch = p.tiles * 128;
+  return p;
+}
+
+// Parts of K for a product of `tiles` pair tiles of `steps` 128-deep steps
+// (0.58 us each) beside `others` steps of the same launch: what the longest
+// pair of CTAs takes, plus the parts' way through memory (8 bytes a result and
+// part at 5 TB/s, and 3 us for the join).
+static int pair_parts(int64_t tiles, int64_t steps, int64_t others, int64_t M, int64_t N) {
+  const int64_t pairs = kPlanSms / 2;
+  double best = 0;
+  int parts = 1;
+  for (int n = 1; n <= 16 && n <= steps; ++n) {
+    const int64_t chain = (steps + n - 1) / n;
+    int64_t longest = (tiles * n + pairs - 1) / pairs * chain;
+    if (others > 0) {
+      const int64_t fair = (tiles * steps + others + pairs - 1) / pairs;
+      longest = chain > fair ? chain : fair;
+    }
+    const double us = 0.58 * static_cast<double>(longest) +
+                      (n > 1 ? 3.0 + 8.0 * n * static_cast<double>(M) * static_cast<double>(N) / 5e6 : 0.0);
+    if (n == 1 || us < best) {
+      best = us;
+      parts = n;
+    }
+  }
+  return parts;
+}
+
+static int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+struct FfnPlan {
+  bool tc = false, skinny = false;     // sizes for the tensor cores; few rows
+  SkinnyPlan up, down;
+  int parts = 1, part_rows = 0;        // of y (forward) or dx (backward)
+  size_t plane = 0;                    // bytes of a [T, F] operand
+  size_t off_counter = 0, off_part = 0, total = 0;
+};
+
+static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, bool backward) {
+  FfnPlan p;
+  p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 : 4);
+  p.off_counter = align256((backward ? 3 : 1) * p.plane);
+  p.off_part = p.off_counter + 256;
+  p.total = p.off_part;
+  p.tc = dtype == RKL_BF16 && H % 8 == 0 && F % 8 == 0 && O % 8 == 0 && T > 0;
+  if (!p.tc) return p;
+  p.part_rows = static_cast<int>((T + 31) / 32 * 32);
+  if (backward) {
+    const int64_t mt = tiles_of(T, 256), steps_t = tiles_of(T, 128);
+    const int64_t others =
+        (2 * tiles_of(F, 256) * tiles_of(H, 256) + tiles_of(O, 256) * tiles_of(F, 256)) * steps_t;
+    p.parts = pair_parts(mt * tiles_of(H, 256), 2 * tiles_of(F, 128), others, T, H);
+    if (p.parts > 1) p.total += size_t(p.parts) * p.part_rows * H * 4;
+    return p;
+  }
+  p.skinny = T <= kFfnSkinnyRows;
+  if (p.skinny) {
+    p.up = skinny_plan(F, F, H);
+    p.down = skinny_plan(O, 0, F);
+    const size_t up = size_t(p.up.parts) * T * p.up.pitch * 4, down = size_t(p.down.parts) * T * p.down.pitch * 4;
+    p.total += up > down ? up : down;
+    return p;
+  }
+  p.parts = pair_parts(tiles_of(T, 256) * tiles_of(O, 256), tiles_of(F, 128), 0, T, O);
+  if (p.parts > 1) p.total += size_t(p.parts) * p.part_rows * O * 4;
+  return p;
+}
+
+// Map of a bf16 operand: `rows` x `cols` row-major, read K-major (K = columns)
+// or MN-major (K = rows).
+static rkl_status operand_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool mn) {
+  return make_map(m, p, false, cols, rows, cols * 2, kBK, mn ? kBK : 128);
+}
+
+// One product of a launch's list: A and B row-major as they lie, `*_mn` where K
+// is their row index.
+static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bool a_mn, const void* B, const void* B2,
+                               bool b_mn, void* C, int64_t M, int64_t N, int64_t K, bool up, int parts, int part_rows) {
+  FfnPairProduct& p = a.p[a.n++];
+  RKL_TRY(operand_map(&p.a[0], A, a_mn ? K : M, a_mn ? M : K, a_mn));
+  RKL_TRY(operand_map(&p.a[1], A2 ? A2 : A, a_mn ? K : M, a_mn ? M : K, a_mn));
+  RKL_TRY(operand_map(&p.b[0], B, b_mn ? K : N, b_mn ? N : K, b_mn));
+  RKL_TRY(operand_map(&p.b[1], B2 ? B2 : B, b_mn ? K : N, b_mn ? N : K, b_mn));
+  if (parts > 1)
+    RKL_TRY(make_map(&p.c, C, true, N, int64_t(parts) * part_rows, N * 4, 32, 32));
+  else
+    RKL_TRY(make_map(&p.c, C, false, N, M, N * 2, 64, 32));
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.mt = static_cast<int>(tiles_of(M, 256));
+  p.nt = static_cast<int>(tiles_of(N, up ? 128 : 256));
+  p.steps = static_cast<int>(tiles_of(K, 128));
+  p.segments = A2 ? 2 : 1;
+  p.a_mn = a_mn;
+  p.b_mn = b_mn;
+  p.parts = parts;
+  p.part_rows = part_rows;
+  p.first = a.items;
+  a.items += p.mt * p.nt * parts;
+  return RKL_OK;
+}
+
+static rkl_status skinny_product(const SkinnyPlan& p, const void* x, const void* W1, int64_t R1, const void* W2, int64_t T,
+                                 int64_t K, float* part, cudaStream_t s) {
+  FfnSkinnyArgs a = {};
+  a.cols = static_cast<int>((T + 15) / 16 * 16);
+  RKL_TRY(operand_map(&a.w1, W1, R1, K, false));
+  RKL_TRY(operand_map(&a.w2, W2 ? W2 : W1, R1, K, false));
+  RKL_TRY(make_map(&a.x, x, false, K, T, K * 2, kBK, a.cols));
+  a.part = part;
+  a.per = p.per;
+  a.tiles = p.tiles;
+  a.tiles_first = p.tiles_first;
+  a.steps = p.steps;
+  a.T = static_cast<int>(T);
+  a.pitch = p.pitch;
+  a.parts = p.parts;
+  RKL_CUDA(launch_ffn_skinny(a, p.grid, s));
+  return RKL_OK;
+}
+
+static FfnJoinArgs join_args(const float* part, void* out, int64_t T, int64_t N) {
+  FfnJoinArgs j = {};
+  j.part = part;
+  j.out = static_cast<uint16_t*>(out);
+  j.T = static_cast<int>(T);
+  j.N = static_cast<int>(N);
+  return j;
+}
+
+static rkl_status join_skinny(const SkinnyPlan& p, int act, const float* part, void* out, float* saved, int64_t T,
+                              int64_t N, cudaStream_t s) {
+  FfnJoinArgs j = join_args(part, out, T, N);
+  j.saved = saved;
+  j.pitch = p.pitch;
+  j.slab = T * p.pitch;
+  j.per = p.per;
+  j.second = p.tiles_first * 128;
+  j.steps = p.steps;
+  RKL_CUDA(launch_ffn_join(act, j, s));
+  return RKL_OK;
+}
+
+static rkl_status join_pair(const FfnPlan& p, const float* part, void* out, int64_t T, int64_t N, cudaStream_t s) {
+  FfnJoinArgs j = join_args(part, out, T, N);
+  j.pitch = N;
+  j.slab = int64_t(p.part_rows) * N;
+  j.parts = p.parts;
+  RKL_CUDA(launch_ffn_join(-1, j, s));
+  return RKL_OK;
+}
+
+static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_gate, const void* W_up,
+                                 const void* W_down, int act, int64_t T, int64_t H, int64_t F, int64_t O, void* y,
+                                 float* saved, uint8_t* ws, int sms, cudaStream_t s) {
+  float* part = reinterpret_cast<float*>(ws + p.off_part);
+  if (p.skinny) {
+    RKL_TRY(skinny_product(p.up, x, W_gate, F, W_up, T, H, part, s));
+    RKL_TRY(join_skinny(p.up, act, part, ws, saved, T, F, s));
+    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, T, F, part, s));
+    return join_skinny(p.down, -1, part, y, nullptr, T, O, s);
+  }
+  FfnPairArgs a = {};
+  RKL_TRY(pair_product(a, x, nullptr, false, W_gate, W_up, false, ws, T, F, H, true, 1, 0));
+  a.save = saved != nullptr;
+  if (saved) {
+    RKL_TRY(make_map(&a.c2, saved, true, F, T, F * 4, 32, 32));
+    RKL_TRY(make_map(&a.c3, saved + T * F, true, F, T, F * 4, 32, 32));
+  }
+  RKL_CUDA(launch_ffn_pair(FFN_UP, act, a, sms, s));
+  FfnPairArgs d = {};
+  RKL_TRY(pair_product(d, ws, nullptr, false, W_down, nullptr, false, p.parts > 1 ? static_cast<void*>(part) : y, T, O, F,
+                       false, p.parts, p.part_rows));
+  RKL_CUDA(launch_ffn_pair(FFN_GEMM, act, d, sms, s));
+  return p.parts > 1 ? join_pair(p, part, y, T, O, s) : RKL_OK;
+}
+
+static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W_gate, const void* W_up,
+                                  const void* W_down, int act, int64_t T, int64_t H, int64_t F, int64_t O,
+                                  const void* dy, const float* saved, void* dx, void* dW_gate, void* dW_up,
+                                  void* dW_down, uint8_t* ws, int sms, cudaStream_t s) {
+  void *a_plane = ws, *dg = ws + p.plane, *du = ws + 2 * p.plane;
+  int* counter = reinterpret_cast<int*>(ws + p.off_counter);
+  float* part = reinterpret_cast<float*>(ws + p.off_part);
+  FfnPairArgs a = {};
+  RKL_TRY(pair_product(a, dy, nullptr, false, W_down, nullptr, true, a_plane, T, F, O, false, 1, 0));
+  RKL_TRY(make_map(&a.c2, dg, false, F, T, F * 2, 64, 32));
+  RKL_TRY(make_map(&a.c3, du, false, F, T, F * 2, 64, 32));
+  a.saved = saved;
+  a.zero_counter = counter;
+  RKL_CUDA(launch_ffn_pair(FFN_DGATE, act, a, sms, s));
+  // longest items (K = 2 F) first
+  FfnPairArgs d = {};
+  d.counter = counter;
+  if (dx)
+    RKL_TRY(pair_product(d, dg, du, false, W_gate, W_up, true, p.parts > 1 ? static_cast<void*>(part) : dx, T, H, F, false,
+                         p.parts, p.part_rows));
+  if (dW_gate) RKL_TRY(pair_product(d, dg, nullptr, true, x, nullptr, true, dW_gate, F, H, T, false, 1, 0));
+  if (dW_up) RKL_TRY(pair_product(d, du, nullptr, true, x, nullptr, true, dW_up, F, H, T, false, 1, 0));
+  if (dW_down) RKL_TRY(pair_product(d, dy, nullptr, true, a_plane, nullptr, true, dW_down, O, F, T, false, 1, 0));
+  RKL_CUDA(launch_ffn_pair(FFN_GEMM, act, d, sms, s));
+  return dx && p.parts > 1 ? join_pair(p, part, dx, T, H, s) : RKL_OK;
 }
 
 rkl_status rkl_ffn_workspace_size(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, int32_t backward,
                                   size_t* bytes) {
   if (bytes == nullptr) return fail(RKL_ERR_NULL, "bytes is NULL");
   RKL_TRY(check_ffn(dtype, ACT_SILU, T, H, F, O));
-  *bytes = ffn_workspace(dtype, T, F, backward != 0);
+  *bytes = ffn_plan(dtype, T, H, F, O, backward != 0).total;
   return RKL_OK;
 }
 
@@ -1367,14 +1599,17 @@ rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up, 
   RKL_TRY(check_ffn_ptr(x, "x", dtype));
   RKL_TRY(check_ffn_ptr(y, "y", dtype));
   RKL_TRY(check_ptr(saved, "saved", false));
-  const size_t need = ffn_workspace(dtype, T, F, false);
-  if (workspace == nullptr || workspace_bytes < need)
-    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", need);
+  const FfnPlan plan = ffn_plan(dtype, T, H, F, O, false);
+  if (workspace == nullptr || workspace_bytes < plan.total)
+    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", plan.total);
   RKL_TRY(check_ptr(workspace, "workspace"));
   int sms = 0;
   RKL_TRY(device_setup(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == RKL_BF16;
+  if (plan.tc && aligned16(x) && aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(y))
+    return ffn_forward_tc(plan, x, W_gate, W_up, W_down, activation, T, H, F, O, y, saved,
+                          static_cast<uint8_t*>(workspace), sms, s);
   FfnSimtArgs a = {};
   a.n = 1;
   a.act = activation;
@@ -1413,13 +1648,17 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
   RKL_TRY(check_ffn_ptr(x, "x", dtype));
   RKL_TRY(check_ffn_ptr(dy, "dy", dtype));
   RKL_TRY(check_ptr(saved, "saved"));
-  const size_t need = ffn_workspace(dtype, T, F, true);
-  if (workspace == nullptr || workspace_bytes < need)
-    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", need);
+  const FfnPlan plan = ffn_plan(dtype, T, H, F, O, true);
+  if (workspace == nullptr || workspace_bytes < plan.total)
+    return fail(RKL_ERR_WORKSPACE, "workspace is NULL or smaller than %zu bytes", plan.total);
   RKL_TRY(check_ptr(workspace, "workspace"));
   if (!dx && !dW_gate && !dW_up && !dW_down) return RKL_OK;
   int sms = 0;
   RKL_TRY(device_setup(&sms));
+  if (plan.tc && aligned16(x) && aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(dy) &&
+      aligned16(dx) && aligned16(dW_gate) && aligned16(dW_up) && aligned16(dW_down))
+    return ffn_backward_tc(plan, x, W_gate, W_up, W_down, activation, T, H, F, O, dy, saved, dx, dW_gate, dW_up, dW_down,
+                           static_cast<uint8_t*>(workspace), sms, s);
   FfnSimtArgs a = {};
   a.act = activation;
   a.saved = const_cast<float*>(saved);

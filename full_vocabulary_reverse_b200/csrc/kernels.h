@@ -45,6 +45,11 @@ enum KernelId : int {
   K_FFN_UP_SIMT,      // gated block on the CUDA cores: both projections, activation, product
   K_FFN_DGATE_SIMT,   // gated block on the CUDA cores: da and the gradients of g and u
   K_FFN_GEMM_SIMT,    // gated block on the CUDA cores: down projection, dx and weight gradients
+  K_FFN_UP_TC,        // gated block, tcgen05: both projections, activation, product
+  K_FFN_DGATE_TC,     // gated block, tcgen05: da and the gradients of g and u
+  K_FFN_GEMM_TC,      // gated block, tcgen05: down projection, dx and weight gradients
+  K_FFN_SKINNY_TC,    // gated block, tcgen05: projections of few rows (parts)
+  K_FFN_JOIN,         // gated block: parts joined (with the activation after the first half)
   K_COUNT
 };
 
@@ -166,6 +171,8 @@ cudaError_t read_and_clear_device_error(int* code);
 cudaError_t read_and_clear_bounds_tc(int* line);
 cudaError_t read_and_clear_bounds_small(int* line);
 cudaError_t read_and_clear_bounds_optim(int* line);
+cudaError_t read_and_clear_bounds_ffn(int* line);
+cudaError_t read_and_clear_ffn_error(int* code);
 
 // ---------------------------------------------------------------- small kernels
 cudaError_t launch_compact(const uint8_t* mask, long long T, int32_t* row_idx, int32_t* n_dev, cudaStream_t s);
@@ -331,5 +338,46 @@ struct FfnSimtArgs {
   int n, act;
 };
 cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s);
+
+// tcgen05 path (ffn_tc_kernels.cu).
+constexpr int kFfnSkinnyRows = 128;  // rows up to which the weights are the M operand
+struct FfnPairProduct {
+  CUtensorMap a[2], b[2];  // bf16, box {64, 128} K-major or {64, 64} MN-major; FFN_UP: b = Wg, Wu
+  CUtensorMap c;           // bf16 result, box {64, 32}; parts > 1: fp32 [parts * part_rows, N], box {32, 32}
+  int M, N;
+  int mt, nt;              // tiles
+  int steps, segments;     // 128-deep steps of a segment of K; segments of K (1 or 2)
+  int a_mn, b_mn;          // operand lies MN-major
+  int parts, part_rows;    // parts of K; rows of a part (a multiple of 32)
+  int first;               // first work item of the launch's list
+};
+struct FfnPairArgs {
+  FfnPairProduct p[kFfnProducts];
+  CUtensorMap c2, c3;      // FFN_UP: g and u (fp32, box {32, 32}); FFN_DGATE: dg and du (bf16, box {64, 32})
+  const float* saved;      // FFN_DGATE: g and u, [2][M, N]
+  int* counter;            // claims work items (nullable: dealt out)
+  int* zero_counter;       // set to 0 for the next launch (nullable)
+  int n, items, save;
+};
+struct FfnSkinnyArgs {
+  CUtensorMap w1, w2, x;   // weights, box {64, 128}; x, box {64, cols}
+  float* part;             // [parts][T][pitch]
+  long long per;           // steps of a CTA
+  int tiles, tiles_first;  // 128-row tiles in all, and of w1
+  int steps;               // 64-deep steps of a tile
+  int T, cols, pitch, parts, stages;
+};
+struct FfnJoinArgs {
+  const float* part;
+  uint16_t* out;           // [T, N] bf16
+  float* saved;            // gated: g and u [2][T, N] (nullable)
+  long long pitch, slab;   // elements between rows, between parts
+  long long per;           // > 0: parts as ffn_skinny_kernel numbers them; 0: `parts` everywhere
+  int T, N, second, steps, parts;
+};
+cudaError_t ffn_tc_setup();
+cudaError_t launch_ffn_pair(int mode, int act, const FfnPairArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_ffn_skinny(FfnSkinnyArgs a, int grid, cudaStream_t s);
+cudaError_t launch_ffn_join(int act, const FfnJoinArgs& a, cudaStream_t s);  // act -1: a plain sum
 
 }  // namespace rkl

@@ -126,9 +126,11 @@ def test_memory_behind_the_results_is_left_alone(T, H, F, O):
     ins, dy = inputs(T, H, F, O, torch.bfloat16, 9)
     sizes = [(T, O), (T, H), (F, H), (F, H), (O, F)]
     bufs = [torch.full((a * b + 4096,), 5.0, dtype=torch.bfloat16, device="cuda") for a, b in sizes]
-    nbytes = ctypes.c_size_t(0)
     L = rb.lib()
-    L.rkl_ffn_workspace_size(0, T, H, F, O, 1, ctypes.byref(nbytes))
+    need = [ctypes.c_size_t(0), ctypes.c_size_t(0)]
+    for way in (0, 1):  # one workspace for both directions
+        assert L.rkl_ffn_workspace_size(0, T, H, F, O, way, ctypes.byref(need[way])) == 0
+    nbytes = max(need, key=lambda b: b.value)
     ws = torch.full((nbytes.value + 4096,), 7, dtype=torch.uint8, device="cuda")
     saved = torch.full((2 * T * F + 1024,), 5.0, device="cuda")
     p = [rb._ptr(t) for t in ins]
