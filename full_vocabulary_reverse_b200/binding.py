@@ -85,6 +85,7 @@ _SIGS = {
     "rkl_backward_topk_logits": ([_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp,
                                   _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "rkl_ffn_workspace_size": ([_i32, _i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_sz)], _i32),
+    "rkl_ffn_saved_size": ([_i64, _i64, ctypes.POINTER(_i64)], _i32),
     "rkl_ffn_forward": ([_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _i32),
     "rkl_ffn_backward": ([_vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                           _sz, _vp], _i32),

@@ -149,9 +149,10 @@ static EncodeTiledFn encode_fn() {
 }
 
 // 2-D row-major map: `inner` contiguous elements per row, `outer` rows,
-// `pitch` bytes between rows; 128-byte swizzle; out-of-bounds reads give 0.
+// `pitch` bytes between rows; out-of-bounds reads give 0.
 static rkl_status make_map(CUtensorMap* m, const void* ptr, bool f32, uint64_t inner, uint64_t outer,
-                           uint64_t pitch, uint32_t box_inner, uint32_t box_outer) {
+                           uint64_t pitch, uint32_t box_inner, uint32_t box_outer,
+                           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(RKL_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   cuuint64_t dims[2] = {inner, outer};
@@ -160,7 +161,7 @@ static rkl_status make_map(CUtensorMap* m, const void* ptr, bool f32, uint64_t i
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(RKL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llux%llu pitch %llu box %ux%u", (int)r,
                 (unsigned long long)inner, (unsigned long long)outer, (unsigned long long)pitch, box_inner,
@@ -1229,7 +1230,9 @@ rkl_status rkl_adamw_step(int32_t n, void* const* params, const void* const* gra
   a.log_beta1 = static_cast<float>(log(beta1));  // -inf for 0: 1 - b^t = 1
   a.log_beta2 = static_cast<float>(log(beta2));
   a.eps = static_cast<float>(eps);
-  a.max_norm = static_cast<float>(max_norm);
+  a.beta1_64 = beta1;
+  a.beta2_64 = beta2;
+  a.max_norm = max_norm;
   a.seed = seed;
   a.n = 0;
   a.blocks = 0;
@@ -1449,6 +1452,11 @@ static rkl_status operand_map(CUtensorMap* m, const void* p, int64_t rows, int64
   return make_map(m, p, false, cols, rows, cols * 2, kBK, mn ? kBK : 128);
 }
 
+// Map of a bf16 result, stored in 32 x 32 boxes.
+static rkl_status result_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
+  return make_map(m, p, false, cols, rows, cols * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // One product of a launch's list: A and B row-major as they lie, `*_mn` where K
 // is their row index.
 static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bool a_mn, const void* B, const void* B2,
@@ -1461,7 +1469,7 @@ static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bo
   if (parts > 1)
     RKL_TRY(make_map(&p.c, C, true, N, int64_t(parts) * part_rows, N * 4, 32, 32));
   else
-    RKL_TRY(make_map(&p.c, C, false, N, M, N * 2, 64, 32));
+    RKL_TRY(result_map(&p.c, C, M, N));
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.mt = static_cast<int>(tiles_of(M, 256));
@@ -1539,11 +1547,7 @@ static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_
   }
   FfnPairArgs a = {};
   RKL_TRY(pair_product(a, x, nullptr, false, W_gate, W_up, false, ws, T, F, H, true, 1, 0));
-  a.save = saved != nullptr;
-  if (saved) {
-    RKL_TRY(make_map(&a.c2, saved, true, F, T, F * 4, 32, 32));
-    RKL_TRY(make_map(&a.c3, saved + T * F, true, F, T, F * 4, 32, 32));
-  }
+  a.saved = saved;
   RKL_CUDA(launch_ffn_pair(FFN_UP, act, a, sms, s));
   FfnPairArgs d = {};
   RKL_TRY(pair_product(d, ws, nullptr, false, W_down, nullptr, false, p.parts > 1 ? static_cast<void*>(part) : y, T, O, F,
@@ -1561,9 +1565,9 @@ static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   FfnPairArgs a = {};
   RKL_TRY(pair_product(a, dy, nullptr, false, W_down, nullptr, true, a_plane, T, F, O, false, 1, 0));
-  RKL_TRY(make_map(&a.c2, dg, false, F, T, F * 2, 64, 32));
-  RKL_TRY(make_map(&a.c3, du, false, F, T, F * 2, 64, 32));
-  a.saved = saved;
+  RKL_TRY(result_map(&a.c2, dg, T, F));
+  RKL_TRY(result_map(&a.c3, du, T, F));
+  a.saved = const_cast<float*>(saved);
   a.zero_counter = counter;
   RKL_CUDA(launch_ffn_pair(FFN_DGATE, act, a, sms, s));
   // longest items (K = 2 F) first
@@ -1584,6 +1588,13 @@ rkl_status rkl_ffn_workspace_size(rkl_dtype dtype, int64_t T, int64_t H, int64_t
   if (bytes == nullptr) return fail(RKL_ERR_NULL, "bytes is NULL");
   RKL_TRY(check_ffn(dtype, ACT_SILU, T, H, F, O));
   *bytes = ffn_plan(dtype, T, H, F, O, backward != 0).total;
+  return RKL_OK;
+}
+
+rkl_status rkl_ffn_saved_size(int64_t T, int64_t F, int64_t* elements) {
+  if (elements == nullptr) return fail(RKL_ERR_NULL, "elements is NULL");
+  RKL_TRY(check_ffn(RKL_FP32, ACT_SILU, T, 1, F, 1));
+  *elements = 2 * ffn_saved_plane(T, F);
   return RKL_OK;
 }
 

@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kSimtThreads) ffn_simt_kernel(const __grid_con
         float slope;
         put(static_cast<T*>(p.c) + at, act_of(a.act, g, &slope) * u);
         if (a.saved != nullptr) {
-          a.saved[at] = g;
-          a.saved[p.M * p.N + at] = u;
+          const long long sv = ffn_saved_at(m, n, p.N);
+          a.saved[sv] = g;
+          a.saved[ffn_saved_plane(p.M, p.N) + sv] = u;
         }
       }
     } else {
@@ -174,7 +175,8 @@ __global__ void __launch_bounds__(kSimtThreads) ffn_simt_kernel(const __grid_con
         if (n >= p.N) continue;
         const long long at = m * p.N + n;
         if (MODE == FFN_DGATE) {
-          const float g = a.saved[at], u = a.saved[p.M * p.N + at], da = acc[i][j];
+          const long long sv = ffn_saved_at(m, n, p.N);
+          const float g = a.saved[sv], u = a.saved[ffn_saved_plane(p.M, p.N) + sv], da = acc[i][j];
           float slope;
           const float h = act_of(a.act, g, &slope);
           const long long one = p.M * p.N;

@@ -93,25 +93,30 @@ __device__ __forceinline__ Item item_of(const FfnPairArgs& a, int i) {
   return t;
 }
 
-// 64 bf16 of each of 32 rows: 32 packed words of a lane's row into the warp's
-// staging box (128-byte swizzle), then one TMA store.
-__device__ __forceinline__ void store_bf16_box(uint8_t* buf, int lane, const uint32_t* w, const CUtensorMap* map, int x,
-                                               int y, bool inside) {
-  if (lane == 0) bulk_wait_read<0>();
+// 32 bf16 of each of 32 rows: 16 packed words of a lane's row into one half of
+// the warp's staging box (64-byte rows, 64-byte swizzle), then a TMA store.
+// The halves alternate, so a store waits only for the one two boxes back.
+__device__ __forceinline__ void store_bf16_box(uint8_t* buf, int& flip, int lane, const uint32_t* w,
+                                               const CUtensorMap* map, int x, int y, bool inside) {
+  uint8_t* half = buf + flip * (kBox / 2);
+  flip ^= 1;
+  if (lane == 0) bulk_wait_read<1>();
   __syncwarp();
-  const uint32_t row = smem_u32(buf) + lane * 128;
+  const uint32_t row = smem_u32(half) + lane * 64;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    st_shared_v4(row + ((i ^ (lane & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  for (int i = 0; i < 4; ++i)
+    st_shared_v4(row + ((i ^ ((lane >> 1) & 3)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0 && inside && RKL_BOUNDS(x >= 0 && (x & 7) == 0 && y >= 0)) {
-    tma_store_2d(map, buf, x, y);
-    bulk_commit();
+  if (lane == 0) {
+    if (inside && RKL_BOUNDS(x >= 0 && (x & 7) == 0 && y >= 0)) tma_store_2d(map, half, x, y);
+    bulk_commit();  // (an empty group where nothing is stored: the count of boxes stays right)
   }
 }
 
-// 32 fp32 of each of 32 rows, the same way.
+// 32 fp32 of each of 32 rows, through the whole box.  A second, empty group
+// follows: the next bf16 store leaves one group pending, and this one reads both
+// halves.
 __device__ __forceinline__ void store_f32_box(uint8_t* buf, int lane, const float* v, const CUtensorMap* map, int x,
                                               int y, bool inside) {
   if (lane == 0) bulk_wait_read<0>();
@@ -125,6 +130,7 @@ __device__ __forceinline__ void store_f32_box(uint8_t* buf, int lane, const floa
   __syncwarp();
   if (lane == 0 && inside && RKL_BOUNDS(x >= 0 && (x & 3) == 0 && y >= 0)) {
     tma_store_2d(map, buf, x, y);
+    bulk_commit();
     bulk_commit();
   }
 }
@@ -333,6 +339,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
     const uint32_t ring_empty0 = mapa_shared(smem_u32(ring_empty), 0);
     const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
     uint8_t* buf = stg + (warp - 2) * kBox;
+    int flip = 0;  // half of the box that the next bf16 store takes
     for (int i = 0;; ++i) {
       const int slot = i % kRing;
       bool ok = mbar_wait_cluster(&ring_full[slot], (i / kRing) & 1, abort_flag);
@@ -364,7 +371,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
         if (lane == 0) mbar_arrive_cluster(acc_empty0 + acc * 8);
       };
       if (EPI == FFN_UP) {
-        uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = half * 64 + c * 32;
@@ -374,56 +380,56 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           tmem_ld_32x32(tb + 128 + col, u);
           tmem_wait_ld();
           if (c == 1) release();
-          if (a.save) {
-            store_f32_box(buf, lane, g, &a.c2, x, row0, live && x < p.N);
-            store_f32_box(buf, lane, u, &a.c3, x, row0, live && x < p.N);
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[c * 16 + e] = pack_bf16x2(act_only<ACT, true>(g[2 * e]) * u[2 * e],
-                                        act_only<ACT, true>(g[2 * e + 1]) * u[2 * e + 1]);
-        }
-        const int x = it.n * 128 + half * 64;
-        store_bf16_box(buf, lane, w, &p.c, x, row0, live && x < p.N);
-      } else if (EPI == FFN_DGATE) {
-        const long long row = row0 + lane;
-        const float* gp = a.saved + row * p.N;
-        const float* up = gp + static_cast<long long>(p.M) * p.N;
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          uint32_t wa[32], wg[32], wu[32];
-          const int x0 = it.n * 256 + half * 128 + b * 64;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int x = x0 + c * 32;
-            float4 g[8], u[8];
+          const bool in = live && x < p.N;
+          if (a.saved != nullptr && in) {
+            float* sg = a.saved + ffn_saved_at(row0 + lane, x, p.N);
+            float* su = sg + ffn_saved_plane(p.M, p.N);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const bool in = row < p.M && x + 4 * e < p.N;  // N is a multiple of 8
-              g[e] = in ? __ldcs(reinterpret_cast<const float4*>(gp + x + 4 * e)) : make_float4(0, 0, 0, 0);
-              u[e] = in ? __ldcs(reinterpret_cast<const float4*>(up + x + 4 * e)) : make_float4(0, 0, 0, 0);
-            }
-            float da[32];
-            tmem_ld_32x32(tb + half * 128 + b * 64 + c * 32, da);
-            tmem_wait_ld();
-            if (b == 1 && c == 1) release();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float* gg = reinterpret_cast<const float*>(g);
-              const float* uu = reinterpret_cast<const float*>(u);
-              float s0, s1;
-              const float h0 = act_with_slope<ACT, true>(gg[2 * e], &s0);
-              const float h1 = act_with_slope<ACT, true>(gg[2 * e + 1], &s1);
-              const float d0 = da[2 * e], d1 = da[2 * e + 1], u0 = uu[2 * e], u1 = uu[2 * e + 1];
-              wa[c * 16 + e] = pack_bf16x2(h0 * u0, h1 * u1);
-              wg[c * 16 + e] = pack_bf16x2(d0 * u0 * s0, d1 * u1 * s1);
-              wu[c * 16 + e] = pack_bf16x2(d0 * h0, d1 * h1);
+              __stcs(reinterpret_cast<float4*>(sg + e * 128), make_float4(g[4 * e], g[4 * e + 1], g[4 * e + 2], g[4 * e + 3]));
+              __stcs(reinterpret_cast<float4*>(su + e * 128), make_float4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]));
             }
           }
-          const bool in = live && x0 < p.N;
-          store_bf16_box(buf, lane, wa, &p.c, x0, row0, in);
-          store_bf16_box(buf, lane, wg, &a.c2, x0, row0, in);
-          store_bf16_box(buf, lane, wu, &a.c3, x0, row0, in);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(act_only<ACT, true>(g[2 * e]) * u[2 * e],
+                               act_only<ACT, true>(g[2 * e + 1]) * u[2 * e + 1]);
+          store_bf16_box(buf, flip, lane, w, &p.c, x, row0, in);
+        }
+      } else if (EPI == FFN_DGATE) {
+        const long long plane = ffn_saved_plane(p.M, p.N);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = half * 128 + c * 32;
+          const int x = it.n * 256 + col;
+          const bool in = live && x < p.N;
+          const float* sg = a.saved + ffn_saved_at(row0 + lane, x, p.N);
+          const float* su = sg + plane;
+          float g[32], u[32], da[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(g + 4 * e) = in ? __ldcs(reinterpret_cast<const float4*>(sg + e * 128)) : z;
+            *reinterpret_cast<float4*>(u + 4 * e) = in ? __ldcs(reinterpret_cast<const float4*>(su + e * 128)) : z;
+          }
+          tmem_ld_32x32(tb + col, da);
+          tmem_wait_ld();
+          if (c == 3) release();
+          uint32_t wa[16], wg[16], wu[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float s0, s1;
+            const float h0 = act_with_slope<ACT, true>(g[2 * e], &s0);
+            const float h1 = act_with_slope<ACT, true>(g[2 * e + 1], &s1);
+            const float d0 = da[2 * e], d1 = da[2 * e + 1], u0 = u[2 * e], u1 = u[2 * e + 1];
+            wa[e] = pack_bf16x2(h0 * u0, h1 * u1);
+            wg[e] = pack_bf16x2(d0 * u0 * s0, d1 * u1 * s1);
+            wu[e] = pack_bf16x2(d0 * h0, d1 * h1);
+          }
+          store_bf16_box(buf, flip, lane, wa, &p.c, x, row0, in);
+          store_bf16_box(buf, flip, lane, wg, &a.c2, x, row0, in);
+          store_bf16_box(buf, flip, lane, wu, &a.c3, x, row0, in);
         }
       } else {
 #pragma unroll 1
@@ -443,7 +449,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
             uint32_t w[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-            store_bf16_box(buf, lane, w, &p.c, x, row0, live && x < p.N);
+            store_bf16_box(buf, flip, lane, w, &p.c, x, row0, live && x < p.N);
+            store_bf16_box(buf, flip, lane, w + 16, &p.c, x + 32, row0, live && x + 32 < p.N);
           }
         }
       }
@@ -678,8 +685,9 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ F
   if (GATED) {
     const float4 u = sum_parts(a, row, a.second + col);
     if (a.saved != nullptr) {
-      *reinterpret_cast<float4*>(a.saved + at) = v;
-      *reinterpret_cast<float4*>(a.saved + static_cast<long long>(a.T) * a.N + at) = u;
+      float* sg = a.saved + ffn_saved_at(row, col, a.N);
+      *reinterpret_cast<float4*>(sg) = v;
+      *reinterpret_cast<float4*>(sg + ffn_saved_plane(a.T, a.N)) = u;
     }
     v.x = act_only<ACT, true>(v.x) * u.x;
     v.y = act_only<ACT, true>(v.y) * u.y;

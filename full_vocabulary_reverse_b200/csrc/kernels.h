@@ -300,7 +300,8 @@ struct AdamwArgs {
   int32_t* control;        // [steps done, ticket]
   const float* norm;       // global gradient norm (nullable)
   const float* lr_dev;     // learning rate on the device (nullable: lr)
-  float lr, beta1, beta2, omb1, omb2, log_beta1, log_beta2, eps, max_norm;
+  float lr, beta1, beta2, omb1, omb2, log_beta1, log_beta2, eps;
+  double beta1_64, beta2_64, max_norm;
   uint32_t seed;
   int advance;             // the step's last launch: counts the step
 };
@@ -322,6 +323,21 @@ cudaError_t launch_norm_final(const double* partial, int n, float* norm, cudaStr
 
 // ---------------------------------------------------------------- gated feed-forward block
 enum : int { FFN_UP = 0, FFN_DGATE = 1, FFN_GEMM = 2 };  // what a product's results go through
+
+// g and u between the forward and the backward pass: fp32, in blocks of 32
+// rows x 32 columns (row blocks outermost), a block as 8 groups of 4 columns x
+// 32 rows x 4 columns.  A warp that holds a row of the block in each lane, as
+// the accumulators come, moves 512 contiguous bytes an access.  u lies
+// ffn_saved_plane(T, F) elements behind g.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline long long ffn_saved_plane(long long T, long long F) { return (T + 31) / 32 * 32 * ((F + 31) / 32 * 32); }
+#ifdef __CUDACC__
+__device__ __forceinline__ long long ffn_saved_at(long long row, long long col, long long F) {
+  return (row / 32 * ((F + 31) / 32) + col / 32) * 1024 + col % 32 / 4 * 128 + row % 32 * 4 + col % 4;
+}
+#endif
 // C(m, n) = sum over segments and k of A_s(m, k) B_s(k, n), row-major C [M, N].
 // FFN_UP: b[0] and b[1] are the gate and up weights, c = act(g) u.
 // FFN_DGATE: c receives a, dg and du, [3][M, N].
@@ -334,7 +350,7 @@ struct FfnProduct {
 constexpr int kFfnProducts = 4;
 struct FfnSimtArgs {
   FfnProduct p[kFfnProducts];
-  float* saved;  // g and u, fp32 [2][M, N] (FFN_UP: nullable)
+  float* saved;  // g and u (FFN_UP: nullable)
   int n, act;
 };
 cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s);
@@ -343,7 +359,7 @@ cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStr
 constexpr int kFfnSkinnyRows = 128;  // rows up to which the weights are the M operand
 struct FfnPairProduct {
   CUtensorMap a[2], b[2];  // bf16, box {64, 128} K-major or {64, 64} MN-major; FFN_UP: b = Wg, Wu
-  CUtensorMap c;           // bf16 result, box {64, 32}; parts > 1: fp32 [parts * part_rows, N], box {32, 32}
+  CUtensorMap c;           // bf16 result, box {32, 32}, 64-byte swizzle; parts > 1: fp32 [parts * part_rows, N], box {32, 32}
   int M, N;
   int mt, nt;              // tiles
   int steps, segments;     // 128-deep steps of a segment of K; segments of K (1 or 2)
@@ -353,11 +369,11 @@ struct FfnPairProduct {
 };
 struct FfnPairArgs {
   FfnPairProduct p[kFfnProducts];
-  CUtensorMap c2, c3;      // FFN_UP: g and u (fp32, box {32, 32}); FFN_DGATE: dg and du (bf16, box {64, 32})
-  const float* saved;      // FFN_DGATE: g and u, [2][M, N]
+  CUtensorMap c2, c3;      // FFN_DGATE: dg and du, as c
+  float* saved;            // g and u (FFN_UP: nullable)
   int* counter;            // claims work items (nullable: dealt out)
   int* zero_counter;       // set to 0 for the next launch (nullable)
-  int n, items, save;
+  int n, items;
 };
 struct FfnSkinnyArgs {
   CUtensorMap w1, w2, x;   // weights, box {64, 128}; x, box {64, cols}
@@ -370,7 +386,7 @@ struct FfnSkinnyArgs {
 struct FfnJoinArgs {
   const float* part;
   uint16_t* out;           // [T, N] bf16
-  float* saved;            // gated: g and u [2][T, N] (nullable)
+  float* saved;            // gated: g and u (nullable)
   long long pitch, slab;   // elements between rows, between parts
   long long per;           // > 0: parts as ffn_skinny_kernel numbers them; 0: `parts` everywhere
   int T, N, second, steps, parts;

@@ -19,7 +19,7 @@
 // tensors travel in the kernel's parameters (up to kOptTensors a launch), so a
 // step needs no copy to the device and can be captured in a graph.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "bounds.cuh"
 #include "kernels.h"
@@ -127,6 +127,9 @@ __device__ __forceinline__ int find_tensor(const int* first, int n, int block) {
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyBlock = 7.888609e-31f;  // 2^-100: a block no larger than this is held as zeros (its scale's
                                              // reciprocal would leave the range of fp32)
+constexpr float kLargeV = 16384.f;
+constexpr float kUlp = 5.9604645e-8f;        // 2^-24
+constexpr uint32_t kVNear = 24u << 4;        // fp32's error of v's place between two codes, in 2^-24 of the way
 
 // The final mix of MurmurHash3 (Austin Appleby, public domain).
 __device__ __forceinline__ uint32_t mix32(uint32_t h) {
@@ -137,10 +140,28 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-__device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
-  __nv_fp8_e4m3 c;
-  c.__x = static_cast<__nv_fp8_storage_t>(code);
-  return static_cast<float>(c);
+// e4m3 codes to floats (every value is one of fp16 too).
+__device__ __forceinline__ void unpack_e4m3x8(uint2 q, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t two = static_cast<uint16_t>(i < 2 ? q.x >> (16 * i) : q.y >> (16 * (i - 2)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The four words' top bytes.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
 // Two floats to two e4m3 codes, to nearest (ties to even), saturating.
@@ -149,13 +170,6 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-
-__device__ __forceinline__ void unpack_e4m3x8(uint2 q, float scale, float* v) {
-  const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = e4m3_to_f32((w[i >> 2] >> (8 * (i & 3))) & 0xffu) * scale;
-}
-
 __device__ __forceinline__ uint2 pack_e4m3x8(const float* v) {
   uint2 q;
   q.x = pack_e4m3(v[0], v[1]) | (pack_e4m3(v[2], v[3]) << 16);
@@ -163,32 +177,42 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float* v) {
   return q;
 }
 
-// Largest magnitude of the warp's 256 values.  Magnitudes are compared as
-// integers, which orders them as floats do and puts a NaN above all, so a NaN
-// reaches the scale instead of vanishing.
-__device__ __forceinline__ float warp_absmax(const float* v) {
-  uint32_t b = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) b = max(b, __float_as_uint(v[e]) & 0x7fffffffu);
-  return __uint_as_float(__reduce_max_sync(kAll, b));
+// Largest of the warp's magnitudes, whose bits are ordered as integers; a NaN
+// is above all, so it reaches the scale instead of vanishing.
+__device__ __forceinline__ float warp_max_magnitude(float v) {
+  return __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(v)));
 }
 
-// r in [0, 448] up or down to an e4m3 value: up with the probability of the
-// rest, by the 20 random bits of h.  e4m3 keeps 3 of fp32's 23 mantissa bits
-// in the normal range, so adding 20 random bits below them and cutting carries
-// exactly when rest + random >= 1; below 2^-6 the values are 2^-9 apart.  A
-// positive r never becomes 0: a second moment of 0 beside a first moment that
-// is not would blow the next update up.
-__device__ __forceinline__ float stochastic_e4m3(float r, uint32_t h) {
-  const uint32_t rnd = h >> 12;
-  float q;
-  if (r >= 0.015625f) {
-    q = __uint_as_float((__float_as_uint(r) + rnd) & 0xfff00000u);
-  } else {
-    q = floorf(fmaf(r, 512.f, static_cast<float>(rnd) * 9.5367431640625e-7f)) * 0.001953125f;
-    if (r > 0.f) q = fmaxf(q, 0.001953125f);
-  }
-  return r != r ? r : fminf(q, kE4m3Max);
+// One element's moments in 64 bits (a block that holds a value too near the
+// border of two codes for fp32 to tell takes these; see below).
+__device__ __forceinline__ double e4m3_to_f64(uint32_t code) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code & 0xffu)));
+  return static_cast<double>(__half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffffu))));
+}
+struct Exact {
+  double beta1, beta2, clip, m_scale, v_scale;
+};
+__device__ __noinline__ double exact_m(const Exact& x, uint32_t code, float grad) {
+  return x.beta1 * (e4m3_to_f64(code) * x.m_scale) + (1 - x.beta1) * (grad * x.clip);
+}
+__device__ __noinline__ double exact_v(const Exact& x, uint32_t code, float grad) {
+  const double g = grad * x.clip;
+  return x.beta2 * (e4m3_to_f64(code) * x.v_scale) + (1 - x.beta2) * g * g;
+}
+// The step between e4m3 values at r >= 0: 2^(exponent - 3), 2^-9 at least.
+__device__ __forceinline__ double e4m3_step(double r) {
+  const long long exponent = max(__double_as_longlong(r) & 0x7ff0000000000000ll, 0x3f90000000000000ll);
+  return __longlong_as_double(exponent - (3ll << 52));
+}
+// 1 / x of a power of two.
+__device__ __forceinline__ double inverse_of(double x) {
+  return __longlong_as_double(0x7fe0000000000000ll - __double_as_longlong(x));
+}
+__device__ __forceinline__ double warp_max(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
+  return v;
 }
 
 }  // namespace
@@ -196,28 +220,34 @@ __device__ __forceinline__ float stochastic_e4m3(float r, uint32_t h) {
 // ============================================================================
 // AdamW
 // ============================================================================
-template <int BITS>
-__global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constant__ AdamwArgs a) {
-  __shared__ float s_step, s_root, s_clip;
-  __shared__ uint32_t s_key;
-  __shared__ int s_skip;
+namespace {
+
+// What every block of a launch needs, found by its first thread.
+struct StepConsts {
+  float step, root, clip, lr;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), gradient scale, learning rate
+  double clip64;
+  uint32_t key;
+  int skip;
+};
+
+__device__ __forceinline__ void begin_step(const AdamwArgs& a, StepConsts* c) {
   if (threadIdx.x == 0) {
     const int t = *reinterpret_cast<volatile int*>(a.control) + 1;
-    float clip = 1.f;
+    double clip = 1;
     int skip = 0;
     if (a.norm != nullptr) {
       const float norm = *a.norm;
-      clip = fminf(1.f, a.max_norm / norm);
       skip = !(norm <= 3.402823466e38f);  // infinity or NaN: the step leaves everything as it is
-      if (norm == 0.f) clip = 1.f;
+      if (norm > 0.f) clip = fmin(1.0, a.max_norm / static_cast<double>(norm));
     }
-    const float lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+    c->lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
     // 1 - b^t = -expm1(t log b) keeps its digits at the first steps
-    s_step = lr / -expm1f(static_cast<float>(t) * a.log_beta1);
-    s_root = rsqrtf(-expm1f(static_cast<float>(t) * a.log_beta2));
-    s_clip = clip;
-    s_skip = skip;
-    s_key = mix32(static_cast<uint32_t>(t) * 0x9E3779B1u + a.seed);
+    c->step = c->lr / -expm1f(static_cast<float>(t) * a.log_beta1);
+    c->root = rsqrtf(-expm1f(static_cast<float>(t) * a.log_beta2));
+    c->clip = static_cast<float>(clip);
+    c->clip64 = clip;
+    c->skip = skip;
+    c->key = mix32(static_cast<uint32_t>(t) * 0x9E3779B1u + a.seed);
     // The step counter moves once, by the block that reads it last: every
     // block has its t before it takes a ticket.
     if (a.advance) {
@@ -229,12 +259,29 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  if (s_skip) return;
-  const float step = s_step, root = s_root, clip = s_clip;
-  const float lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+}
+
+// p from the new moments: square root and quotient by the hardware's
+// approximations (2^-22 each).  The update is lr times smaller than p's own
+// scale, its last bits are lost in p.
+__device__ __forceinline__ float new_param(float p, float m, float v, float keep, float step, float root, float eps) {
+  float sq, inv;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(sq) : "f"(v));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(sq, root, eps)));
+  return fmaf(p, keep, -(step * m) * inv);
+}
+
+}  // namespace
+
+// 32-bit moments.  Bound by memory: 30 bytes an element with bf16 parameters,
+// master copies and fp32 gradients.
+__global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constant__ AdamwArgs a) {
+  __shared__ StepConsts k;
+  begin_step(a, &k);
+  if (k.skip) return;
+  const float step = k.step, root = k.root, clip = k.clip, lr = k.lr;
   const int lane = threadIdx.x & 31;
-  int t = -1;
-  int t_end = 0;
+  int t = -1, t_end = 0;
   for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < a.blocks; b += gridDim.x * kWarps) {
     if (t < 0 || b >= t_end) {
       t = find_tensor(a.first, a.n, b);
@@ -252,53 +299,179 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
       ld8_f32(master, p);
     else
       load8(x.param, x.flags & OPT_PARAM_BF16, x.flags & OPT_WIDE_PARAM, i, x.n, p);
-    const long long q = s / kOptBlock;  // the block's scale
-    if (BITS == 32) {
-      ld8_f32(static_cast<const float*>(a.m) + s, m);
-      ld8_f32(static_cast<const float*>(a.v) + s, v);
-    } else {
-      const uint2 cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + s));
-      const uint2 cv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + s));
-      unpack_e4m3x8(cm, a.m_scale[q], m);
-      unpack_e4m3x8(cv, a.v_scale[q], v);
-    }
+    ld8_f32(static_cast<const float*>(a.m) + s, m);
+    ld8_f32(static_cast<const float*>(a.v) + s, v);
     const float keep = 1.f - lr * x.decay;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float ge = g[e] * clip;
       m[e] = fmaf(a.beta1, m[e], a.omb1 * ge);
       v[e] = fmaf(a.beta2, v[e], a.omb2 * ge * ge);
-      // square root and quotient by the hardware's approximations (2^-22): the
-      // update is lr times smaller than p's own scale, its last bits are lost in p
-      float sq;
-      asm("sqrt.approx.f32 %0, %1;" : "=f"(sq) : "f"(v[e]));
-      p[e] = fmaf(p[e], keep, -__fdividef(step * m[e], fmaf(sq, root, a.eps)));
+      p[e] = new_param(p[e], m[e], v[e], keep, step, root, a.eps);
     }
+    st8_f32(static_cast<float*>(a.m) + s, m);
+    st8_f32(static_cast<float*>(a.v) + s, v);
     if (master != nullptr) st8_f32(master, p);
     store8(x.param, x.flags & OPT_PARAM_BF16, x.flags & OPT_WIDE_PARAM, i, x.n, p);
-    if (BITS == 32) {
-      st8_f32(static_cast<float*>(a.m) + s, m);
-      st8_f32(static_cast<float*>(a.v) + s, v);
-    } else {
-      const float mm = warp_absmax(m), vm = warp_absmax(v);
-      const bool m_some = !(mm <= kTinyBlock), v_some = !(vm <= kTinyBlock);
-      const float mi = m_some ? kE4m3Max / mm : 0.f, vi = v_some ? kE4m3Max / vm : 0.f;
-      // First moment to the nearest code: b1 leaves each step a tenth of a new
-      // value, above the half step of the code.  Second moment stochastically:
-      // with b2 = 0.999 a step moves it by less than half a code's step, and to
-      // the nearest it would never move at all.
-      const uint32_t hi = mix32(s_key + static_cast<uint32_t>(static_cast<unsigned long long>(s) >> 32));
+  }
+}
+
+// 8-bit moments: 8 bytes an element with bf16 parameters and gradients.  The
+// arithmetic (about 70 instructions an element, most of them the codes') and
+// not memory sets the time.
+//
+// Beside the codes, fp32 arithmetic finds the values that lie within its error
+// of a border between two codes; their block then looks at those again in 64
+// bits, so the codes are always the formula's.  With u = 2^-24, r = value 448 /
+// largest:
+//   m: off by 5 u t, t = |b1 m| + |(1 - b1) g|, whatever cancels in it; the
+//      block's largest by as much of its own t, which is below largest +
+//      2 b1 448 scale; r by 5 u more: below t 448 / largest u (10 + 5 W), W that
+//      bound over the largest.
+//   v: all terms are positive: 24 u of r, a code's step is r / 16 at least.
+__global__ void __launch_bounds__(32 * kWarps, 4) adamw8_kernel(const __grid_constant__ AdamwArgs a) {
+  __shared__ StepConsts k;
+  begin_step(a, &k);
+  if (k.skip) return;
+  const int lane = threadIdx.x & 31;
+  int t = -1, t_end = 0;
+  for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < a.blocks; b += gridDim.x * kWarps) {
+    if (t < 0 || b >= t_end) {
+      t = find_tensor(a.first, a.n, b);
+      t_end = t + 1 < a.n ? a.first[t + 1] : a.blocks;
+    }
+    const AdamwTensor& x = a.t[t];
+    const long long i = static_cast<long long>(b - a.first[t]) * kOptBlock + lane * 8;  // in the tensor
+    const long long s = x.at + i;                                                       // in the state
+    if (!RKL_BOUNDS(i >= lane * 8 && s - lane * 8 + kOptBlock <= a.total && (x.at & (kOptBlock - 1)) == 0)) continue;
+    const long long q = s / kOptBlock;  // the block's scale
+    uint2* cm = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + s);
+    uint2* cv = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + s);
+    const uint2 om = __ldcs(cm), ov = __ldcs(cv);
+    const float ms = a.m_scale[q], vs = a.v_scale[q];
+    float m[8], v[8], term[8];
+    float m_top = 0.f, v_top = 0.f;
+    {
+      float g[8], p[8];
+      load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i, x.n, g);
+      float* master = a.master != nullptr ? a.master + s : nullptr;
+      if (master != nullptr)
+        ld8_f32(master, p);
+      else
+        load8(x.param, x.flags & OPT_PARAM_BF16, x.flags & OPT_WIDE_PARAM, i, x.n, p);
+      const float keep = 1.f - k.lr * x.decay;
+      const float mk = a.beta1 * ms, vk = a.beta2 * vs;
+      unpack_e4m3x8(om, m);
+      unpack_e4m3x8(ov, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        m[e] *= mi;
-        v[e] = stochastic_e4m3(fminf(v[e] * vi, kE4m3Max), mix32(static_cast<uint32_t>(s + e) ^ hi));
+        const float ge = g[e] * k.clip;
+        const float m1 = m[e] * mk, m2 = a.omb1 * ge;
+        m[e] = m1 + m2;
+        term[e] = fabsf(m1) + fabsf(m2);
+        v[e] = fmaf(a.omb2 * ge, ge, v[e] * vk);
+        p[e] = new_param(p[e], m[e], v[e], keep, k.step, k.root, a.eps);
       }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + s) = pack_e4m3x8(m);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + s) = pack_e4m3x8(v);
-      if (lane == 0) {
-        a.m_scale[q] = m_some ? mm / kE4m3Max : 0.f;
-        a.v_scale[q] = v_some ? vm / kE4m3Max : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        m_top = max3_nan(m_top, fabsf(m[e]), fabsf(m[e + 1]));
+        v_top = max3_nan(v_top, v[e], v[e + 1]);
       }
+      if (master != nullptr) st8_f32(master, p);
+      store8(x.param, x.flags & OPT_PARAM_BF16, x.flags & OPT_WIDE_PARAM, i, x.n, p);
+    }
+    const float mm = warp_max_magnitude(m_top), vm = warp_max_magnitude(v_top);
+    const bool m_some = !(mm <= kTinyBlock), v_some = !(vm <= kTinyBlock);
+    const float mi = m_some ? __fdividef(kE4m3Max, mm) : 0.f, vi = v_some ? __fdividef(kE4m3Max, vm) : 0.f;
+    const bool far = vm > kLargeV;  // vi 2^-120 leaves fp32's normal range: all of v in 64 bits
+    const float vi120 = vi * 7.52316384526264e-37f;
+    const uint32_t least = v_some ? 0x01000000u : 0u;
+    // First moment to the nearest code: b1 leaves each step a tenth of a new
+    // value, above the half step of the code.  Second moment stochastically:
+    // with b2 = 0.999 a step moves it by less than half a code's step, and to
+    // the nearest it would never move at all.
+    const float w = fmaf(896.f * a.beta1, ms, mm) * mi * (1.f / kE4m3Max);
+    const float off = mi * kUlp * fmaf(5.f, w, 10.f);
+    const uint32_t place =
+        static_cast<uint32_t>(s) ^ mix32(k.key + static_cast<uint32_t>(static_cast<unsigned long long>(s) >> 32));
+    // How much further |m| lies from the border next to it than fp32's error:
+    // half the code's step less the distance to the code.  The step is 2^-3 of
+    // 2^exponent (that of the smallest normal code at least); adding 2^20 times
+    // 2^exponent rounds to a multiple of it.
+    auto clear_of_border = [&](float me, float te) {
+      const float r = fabsf(me);
+      const float top = fmaxf(__uint_as_float(__float_as_uint(r) & 0x7f800000u), 0.015625f);
+      const float rest = r - (fmaf(top, 1048576.f, r) - top * 1048576.f);
+      return fmaf(te, -off, fmaf(top, 0.0625f, -fabsf(rest)));
+    };
+    // r 2^-120 has e4m3's exponent and mantissa above 20 more bits; 16 times
+    // them the code is the top byte, and adding 24 random bits (20 and 4 that
+    // cannot matter) carries into it exactly when rest + random >= 1.
+    auto raised = [&](float ve, int e) {
+      const uint32_t h = mix32(place ^ static_cast<uint32_t>(e));
+      return __float_as_uint(ve * vi120) * 16u + (h >> 8);
+    };
+    auto v_window = [](uint32_t y) { return y * 256u + (kVNear << 8); };  // below 2 kVNear << 8: next to a border
+    float nearest_m = 1.f;
+    uint32_t nearest_v = 0xffffffffu, y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      m[e] *= mi;
+      nearest_m = fminf(nearest_m, clear_of_border(m[e], term[e]));
+      y[e] = raised(v[e], e);
+      nearest_v = min(nearest_v, v_window(y[e]));
+      // not to 0 from above it: a second moment of 0 beside a first moment that
+      // is not would blow the next update up.  (The largest value's carry out of
+      // the last code is next to a border.)
+      y[e] = max(y[e], min(__float_as_uint(v[e]), 1u) * least);
+    }
+    const bool near_m = __any_sync(kAll, nearest_m <= 0.f);
+    const bool near_v = far || __any_sync(kAll, nearest_v < (kVNear << 9));
+    if (near_m || near_v) {
+      const Exact z{a.beta1_64, a.beta2_64, k.clip64, ms, vs};
+      float g[8];
+      load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i, x.n, g);
+      if (near_m) {
+        double most = 0;  // among those that may be the largest
+        const float least_r = kE4m3Max * fmaf(w, -16.f * kUlp, 1.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!(fabsf(m[e]) < least_r)) most = fmax(most, fabs(exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e])));
+        most = warp_max(most);
+        const double inv = m_some ? 448.0 / most : 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (clear_of_border(m[e], term[e]) <= 0.f) {
+            const double r = exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e]) * inv;
+            const double gap = e4m3_step(fabs(r));
+            m[e] = static_cast<float>(rint(r * inverse_of(gap)) * gap);
+          }
+      }
+      if (near_v) {
+        double most = 0;
+        const float least_r = far ? 0.f : kE4m3Max * (1.f - 32.f * kUlp);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!(v[e] * vi < least_r)) most = fmax(most, exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]));
+        most = warp_max(most);
+        const double inv = v_some ? 448.0 / most : 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (far || v_window(raised(v[e], e)) < (kVNear << 9)) {
+            const double r = exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]) * inv;
+            const double gap = e4m3_step(r);
+            const double up =
+                floor(r * inverse_of(gap) + (mix32(place ^ static_cast<uint32_t>(e)) >> 12) * 9.5367431640625e-7) * gap;
+            const uint32_t code = __float_as_uint(static_cast<float>(up) * 7.52316384526264e-37f) >> 20;
+            y[e] = min(max(code, r > 0 ? 1u : 0u), 126u) << 24;
+          }
+      }
+    }
+    *cv = make_uint2(top_bytes(y[0], y[1], y[2], y[3]), top_bytes(y[4], y[5], y[6], y[7]));
+    *cm = pack_e4m3x8(m);
+    if (lane == 0) {
+      a.m_scale[q] = m_some ? mm * (1.f / kE4m3Max) : 0.f;
+      a.v_scale[q] = v_some ? vm * (1.f / kE4m3Max) : 0.f;
     }
   }
 }
@@ -351,12 +524,36 @@ __global__ void __launch_bounds__(32 * kWarps) norm_partial_kernel(const __grid_
     const NormTensor& x = a.t[t];
     const long long i = static_cast<long long>(b - a.first[t]) * kNormChunk + lane * 8;
     if (!RKL_BOUNDS(i >= 0 && i < x.n + kNormChunk)) continue;
-    float v[4][8];
+    // A chunk inside the tensor: all its loads are in flight before the first
+    // sum (behind a test each, they went one by one: 3.7 TB/s).
+    if ((x.flags & OPT_WIDE_GRAD) && i - lane * 8 + kNormChunk <= x.n) {
+      if (x.flags & OPT_GRAD_BF16) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x.grad) + i);
+        uint4 q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i + 256 * j, x.n, v[j]);
+        for (int j = 0; j < 4; ++j) q[j] = __ldcs(p + 32 * j);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum += sum_squares(v[j]);
+        for (int j = 0; j < 4; ++j) {
+          float v[8];
+          bf16x8_to_f32(q[j], v);
+          sum += sum_squares(v);
+        }
+      } else {
+        const float* p = static_cast<const float*>(x.grad) + i;
+        float v[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ld8_f32(p + 256 * j, v[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += sum_squares(v[j]);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[8];
+      load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i + 256 * j, x.n, v);
+      sum += sum_squares(v);
+    }
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) a.partial[blockIdx.x] = sum;
@@ -375,9 +572,9 @@ __global__ void __launch_bounds__(32 * kWarps) norm_final_kernel(const double* p
 cudaError_t launch_adamw(int bits, const AdamwArgs& a, int grid, cudaStream_t s) {
   LaunchScope scope(bits == 8 ? K_ADAMW8 : K_ADAMW, s);
   if (bits == 8)
-    adamw_kernel<8><<<grid, 32 * kWarps, 0, s>>>(a);
+    adamw8_kernel<<<grid, 32 * kWarps, 0, s>>>(a);
   else
-    adamw_kernel<32><<<grid, 32 * kWarps, 0, s>>>(a);
+    adamw_kernel<<<grid, 32 * kWarps, 0, s>>>(a);
   return cudaGetLastError();
 }
 

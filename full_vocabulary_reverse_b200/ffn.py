@@ -43,14 +43,20 @@ def _workspace(x, T, H, F, O, backward):
     return torch.empty(nbytes.value, dtype=torch.uint8, device=x.device)
 
 
+def _saved_size(T, F):
+    n = ctypes.c_int64(0)
+    _check(lib().rkl_ffn_saved_size(T, F, ctypes.byref(n)))
+    return n.value
+
+
 def ffn_forward(x, W_gate, W_up, W_down, activation=ACT_SILU, save=False):
-    """(y [T, O], saved): saved (fp32 [2, T, F], for ``ffn_backward``) is None
-    unless ``save``."""
+    """(y [T, O], saved): saved (fp32, g and u in the library's own order, for
+    ``ffn_backward``) is None unless ``save``."""
     T, H, F, O = _sizes(x, W_gate, W_up, W_down)
     x, W_gate, W_up, W_down = (t.contiguous() for t in (x, W_gate, W_up, W_down))
     with torch.cuda.device(x.device):
         y = torch.empty((T, O), dtype=x.dtype, device=x.device)
-        saved = torch.empty((2, T, F), dtype=torch.float32, device=x.device) if save else None
+        saved = torch.empty(_saved_size(T, F), dtype=torch.float32, device=x.device) if save else None
         ws = _workspace(x, T, H, F, O, 0)
         _check(lib().rkl_ffn_forward(_ptr(x), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _dtype_code(x), activation,
                                      T, H, F, O, _ptr(y), _ptr(saved), _ptr(ws), ws.numel(), _stream(x.device)))
@@ -63,7 +69,7 @@ def ffn_backward(x, W_gate, W_up, W_down, dy, saved, activation=ACT_SILU, needs=
     T, H, F, O = _sizes(x, W_gate, W_up, W_down)
     if dy.shape != (T, O) or dy.device != x.device or dy.dtype != x.dtype:
         raise RKLError(2, "dy must be a [%d, %d] tensor of x's dtype and device" % (T, O))
-    if saved.shape != (2, T, F) or saved.dtype != torch.float32 or saved.device != x.device or not saved.is_contiguous():
+    if saved.shape != (_saved_size(T, F),) or saved.dtype != torch.float32 or saved.device != x.device or not saved.is_contiguous():
         raise RKLError(2, "saved must be what ffn_forward gave for the same sizes")
     x, W_gate, W_up, W_down, dy = (t.contiguous() for t in (x, W_gate, W_up, W_down, dy))
     with torch.cuda.device(x.device):

@@ -435,8 +435,9 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
  * in the backward pass a, dg and du, are rounded once to dtype as operands of
  * the next product.
  *
- * saved: fp32 [2][T, F], g and u for the backward pass (NULL in the forward pass
- * alone: not stored).  The backward pass:
+ * saved: g and u for the backward pass, fp32, rkl_ffn_saved_size elements in an
+ * order of the library's own (NULL in the forward pass alone: not stored).  The
+ * backward pass:
  *
  *     da = dy W_down,  dg = da u act'(g),  du = da act(g)
  *     dx = dg W_gate + du W_up,  dW_gate = dg^T x,  dW_up = du^T x,
@@ -453,6 +454,7 @@ typedef enum rkl_activation {
 
 rkl_status rkl_ffn_workspace_size(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O,
                                   int32_t backward, size_t* bytes /* host out */);
+rkl_status rkl_ffn_saved_size(int64_t T, int64_t F, int64_t* elements /* host out */);
 rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up,
                            const void* W_down, rkl_dtype dtype, int32_t activation,
                            int64_t T, int64_t H, int64_t F, int64_t O, void* y, float* saved,

@@ -68,9 +68,18 @@ def test_workspace_size(L):
     assert L.rkl_ffn_workspace_size(0, 4, 16, 32, 8, 0, ctypes.byref(need)) == 0
     one = need.value
     assert one >= 4 * 32 * 2
-    assert L.rkl_ffn_workspace_size(0, 4, 16, 32, 8, 1, ctypes.byref(need)) == 0 and need.value > one
+    assert L.rkl_ffn_workspace_size(0, 4, 16, 32, 8, 1, ctypes.byref(need)) == 0 and need.value >= 3 * 4 * 32 * 2
+    assert backward(L, nbytes=need.value - 1) == 5
     # the workspace that is asked for is enough, one byte less is not
     assert forward(L, nbytes=one - 1) == 5
+
+
+def test_saved_size(L):
+    n = ctypes.c_int64(0)
+    assert L.rkl_ffn_saved_size(1, 1, None) == 1
+    assert L.rkl_ffn_saved_size(-1, 1, ctypes.byref(n)) == 2
+    assert L.rkl_ffn_saved_size(33, 65, ctypes.byref(n)) == 0 and n.value == 2 * 64 * 96
+    assert L.rkl_ffn_saved_size(0, 65, ctypes.byref(n)) == 0 and n.value == 0
 
 
 def test_python_refusals_without_a_device():
