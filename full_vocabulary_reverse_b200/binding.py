@@ -133,6 +133,27 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _raw_stream(index):
+    """The handle of device `index`'s current stream."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+class _SameDevice:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME_DEVICE = _SameDevice()
+
+
+def _on_device(index):
+    """Makes device `index` current for a while (nothing to do where it is)."""
+    return _SAME_DEVICE if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
 def _dtype_code(t):
     if t.dtype == torch.bfloat16:
         return DT_BF16

@@ -7,15 +7,19 @@
 //   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T a
 //
 // One tiled product kernel does all of them: C(m, n) = sum_k A(m, k) B(k, n)
-// with any strides, 256 threads on a BT x BT tile, 16 deep, the next slice's
-// loads in registers while the present one is multiplied.  A thread owns R x R
-// results (R = BT / 16): rows and columns in groups of 4, BT / 2 apart.  So the
-// up form puts Wg's columns in the tile's first half and Wu's in the second (its
-// groups of columns are R / 2 wide), and a thread holds g and u of the same
-// elements: the activation, the product and the rounding happen in its registers.
+// with any strides, BT x BT tiles, 16 deep, the next slices' loads under way
+// while the present one is multiplied.  A thread owns 8 x 8 results: rows and
+// columns in two groups of 4, BT / 2 apart.  So the up form puts Wg's columns in
+// the tile's first half and Wu's in the second, and a thread holds g and u of
+// the same elements: the activation, the product and the rounding happen in its
+// registers.
 //
-// Bound by the FFMA pipe (128 a clock and SM).  BT = 128 (64 results a thread,
-// 4 16-byte shared loads for 64 FFMA) where its tiles fill the SMs; else 64.
+// Bound by shared memory and the FFMA pipe alike: of a 16-byte read every 8
+// lanes take a cycle, so 8 x 8 results need 16 cycles of reads for 16 cycles of
+// multiply-adds (4 x 4 results a thread, 8 for 4, ran half as fast).  BT = 128
+// where there are many tiles; else 64, whose 64 threads of results are four
+// times over, each for a quarter of every slice, and add up at the end: with
+// one tile an SM, 2 warps alone took twice as long.
 #include <cuda_bf16.h>
 
 #include "ffn_act.cuh"
@@ -25,10 +29,13 @@ namespace rkl {
 namespace {
 
 constexpr int kDepth = 16;
+constexpr int kResults = 8;  // of a thread, each way
 constexpr int kSimtThreads = 256;
+template <int BT>
+constexpr int kGroups = kSimtThreads / ((BT / kResults) * (BT / kResults));  // of threads that share a tile's K
+template <int BT>
+constexpr int kShare = BT * kDepth / kSimtThreads;  // elements of an operand's slice that a thread moves
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -41,52 +48,141 @@ __device__ __forceinline__ float act_of(int act, float g, float* slope) {
   }
 }
 
-// One slice of an operand: BT positions along m (or n) x kDepth along k,
-// element i of a thread's BT / 16.  Neighbouring threads run along the
-// dimension that is contiguous in memory.
-template <typename T, int BT>
-struct Slice {
-  float v[BT / 16];
+// Two fp32 multiply-adds in one instruction: the issue slots that this saves go
+// to the shared-memory reads beside them.
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
 
-  __device__ __forceinline__ static void place(bool k_fast, int i, int* mn, int* k) {
-    const int e = threadIdx.x + i * kSimtThreads;
-    *k = k_fast ? e % kDepth : e / BT;
-    *mn = k_fast ? e / kDepth : e % BT;
-  }
-  // positions [mn0, mn_end) x [k0, k_end) hold values, the others zero
-  __device__ __forceinline__ void load(const T* p, long long s_mn, long long s_k, long long mn0, long long mn_end,
-                                       long long k0, long long k_end, int first, int half) {
-    const bool k_fast = s_k == 1;
+// Where element i of this thread's share of a slice lies: BT positions along m
+// (or n) x kDepth along k.  Neighbouring threads run along the dimension that is
+// contiguous in memory.
+template <int BT>
+__device__ __forceinline__ void slice_place(bool k_fast, int i, int* mn, int* k) {
+  const int e = threadIdx.x + i * kSimtThreads;
+  *k = k_fast ? e % kDepth : e / BT;
+  *mn = k_fast ? e / kDepth : e % BT;
+}
+
+// This thread's share of an operand's slices: position `mn` of the tile is row
+// mn0 + mn of p, or from position `half` on (half > 0) row mn0 + mn - half of
+// p2; rows at mn_end and behind are zero.  Element i of a slice lies offset[i]
+// elements behind the slice's start.
+template <typename T, int BT>
+struct Operand {
+  const T *p, *p2;  // at (mn0, first k of the next slice)
+  long long s_k;
+  int offset[kShare<BT>];
+  uint32_t rows, upper;  // bits: the element's row is there; it comes from p2
+  bool k_fast;
+
+  __device__ __forceinline__ Operand(const void* base, const void* base2, long long s_mn, long long stride_k,
+                                     long long mn0, long long mn_end, int half)
+      : p(static_cast<const T*>(base) + mn0 * s_mn), p2(static_cast<const T*>(base2) + (half > 0 ? mn0 * s_mn : 0)),
+        s_k(stride_k), rows(0), upper(0), k_fast(stride_k == 1) {
 #pragma unroll
-    for (int i = 0; i < BT / 16; ++i) {
+    for (int i = 0; i < kShare<BT>; ++i) {
       int mn, k;
-      place(k_fast, i, &mn, &k);
-      if (half > 0 && (mn < first || mn >= first + half)) continue;  // the other half's operand fills it
-      const long long m = mn0 + mn - first;
-      v[i] = m < mn_end && k0 + k < k_end ? to_f32(p[m * s_mn + (k0 + k) * s_k]) : 0.f;
+      slice_place<BT>(k_fast, i, &mn, &k);
+      const bool second = half > 0 && mn >= half;
+      const int row = second ? mn - half : mn;
+      offset[i] = static_cast<int>(row * s_mn + k * s_k);  // strides are below 2^20: it fits
+      rows |= (mn0 + row < mn_end ? 1u : 0u) << i;
+      upper |= (second ? 1u : 0u) << i;
     }
   }
-  __device__ __forceinline__ void store(float (*s)[BT + 4], bool k_fast) const {
-#pragma unroll
-    for (int i = 0; i < BT / 16; ++i) {
-      int mn, k;
-      place(k_fast, i, &mn, &k);
-      s[k][mn] = v[i];
-    }
+  // element i of the slice with `left` positions along k; *k: its place there
+  __device__ __forceinline__ const T* at(int i, int left, int* mn, int* k, bool* in) const {
+    slice_place<BT>(k_fast, i, mn, k);
+    *in = ((rows >> i) & 1) && *k < left;
+    return ((upper >> i) & 1 ? p2 : p) + offset[i];
+  }
+  __device__ __forceinline__ void advance() {
+    p += kDepth * s_k;
+    p2 += kDepth * s_k;
   }
 };
+
+// fp32: straight into shared memory, 4 bytes at a time (rows need no
+// alignment), zeros where nothing is read.
+template <int BT>
+__device__ __forceinline__ void slice_async(const Operand<float, BT>& o, int left, float (*s)[BT + 4]) {
+#pragma unroll
+  for (int i = 0; i < kShare<BT>; ++i) {
+    int mn, k;
+    bool in;
+    const float* p = o.at(i, left, &mn, &k, &in);
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][mn]));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in ? p : o.p), "r"(in ? 4 : 0) : "memory");
+  }
+}
+
+// bf16: through registers, widened to fp32.
+template <int BT>
+__device__ __forceinline__ void slice_load(const Operand<__nv_bfloat16, BT>& o, int left, float* v) {
+#pragma unroll
+  for (int i = 0; i < kShare<BT>; ++i) {
+    int mn, k;
+    bool in;
+    const __nv_bfloat16* p = o.at(i, left, &mn, &k, &in);
+    v[i] = in ? __bfloat162float(*p) : 0.f;
+  }
+}
+template <int BT>
+__device__ __forceinline__ void slice_store(bool k_fast, const float* v, float (*s)[BT + 4]) {
+#pragma unroll
+  for (int i = 0; i < kShare<BT>; ++i) {
+    int mn, k;
+    slice_place<BT>(k_fast, i, &mn, &k);
+    s[k][mn] = v[i];
+  }
+}
+
+// What element (m, n) goes through: its sum, and in the up form u's.
+template <typename T, int MODE>
+__device__ __forceinline__ void finish(const FfnSimtArgs& a, const FfnProduct& p, long long m, long long n, float sum,
+                                       float u) {
+  const long long at = m * p.N + n;
+  T* c = static_cast<T*>(p.c) + at;
+  float slope;
+  if (MODE == FFN_UP) {
+    put(c, act_of(a.act, sum, &slope) * u);
+    if (a.saved != nullptr) {
+      const long long sv = ffn_saved_at(m, n, p.N);
+      a.saved[sv] = sum;
+      a.saved[ffn_saved_plane(p.M, p.N) + sv] = u;
+    }
+  } else if (MODE == FFN_DGATE) {
+    const long long sv = ffn_saved_at(m, n, p.N), one = p.M * p.N;
+    const float g = a.saved[sv], up = a.saved[ffn_saved_plane(p.M, p.N) + sv];
+    const float h = act_of(a.act, g, &slope);
+    put(c, h * up);                      // a
+    put(c + one, sum * up * slope);      // dg
+    put(c + 2 * one, sum * h);           // du
+  } else {
+    put(c, sum);
+  }
+}
 
 }  // namespace
 
 template <typename T, int BT, int MODE>
-__global__ void __launch_bounds__(kSimtThreads) ffn_simt_kernel(const __grid_constant__ FfnSimtArgs a) {
-  constexpr int R = BT / 16;       // results a thread and dimension
-  constexpr int STEP = BT * 4 / R;  // between a thread's groups of 4 rows
-  constexpr int CW = MODE == FFN_UP ? R / 2 : 4;  // columns of a group: up needs two groups, gates and ups
-  constexpr int CSTEP = BT * CW / R;
+__global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_constant__ FfnSimtArgs a) {
+  constexpr int R = kResults;
+  constexpr int STEP = BT / 2;  // between a thread's groups of 4
   constexpr int BN = MODE == FFN_UP ? BT / 2 : BT;  // result columns of a tile
-  __shared__ __align__(16) float sa[2][kDepth][BT + 4];
-  __shared__ __align__(16) float sb[2][kDepth][BT + 4];
+  constexpr bool kAsync = sizeof(T) == 4;
+  // Slices in flight.  The small tile multiplies a slice in less time than a read
+  // from memory takes: three are under way behind the present one.
+  constexpr int RING = BT == 64 ? 4 : 2;
+  __shared__ __align__(16) float sa[RING][kDepth][BT + 4];
+  __shared__ __align__(16) float sb[RING][kDepth][BT + 4];
+  static_assert(kGroups<BT> == 1 || sizeof(sa) >= size_t(BT) * BT * 4, "a group's sums fit into sa or sb");
 
   int q = 0;
   while (q + 1 < a.n && static_cast<int>(blockIdx.x) >= a.p[q + 1].first_tile) ++q;
@@ -94,98 +190,147 @@ __global__ void __launch_bounds__(kSimtThreads) ffn_simt_kernel(const __grid_con
   const int tile = blockIdx.x - p.first_tile;
   const int n_tiles = static_cast<int>((p.N + BN - 1) / BN);
   const long long m0 = static_cast<long long>(tile / n_tiles) * BT, n0 = static_cast<long long>(tile % n_tiles) * BN;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int group = threadIdx.x / (kSimtThreads / kGroups<BT>);
+  const int tx = threadIdx.x % (BT / R), ty = threadIdx.x / (BT / R) % (BT / R);
+
+  uint64_t acc2[R][R / 2];  // neighbouring columns in pairs
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < R / 2; ++j) acc2[i][j] = 0;
+
+  Operand<T, BT> oa(p.a[0], nullptr, p.sam, p.sak, m0, p.M, 0);
+  Operand<T, BT> ob(p.b[0], p.b[1], p.sbn, p.sbk, n0, p.N, MODE == FFN_UP ? BN : 0);
+  // Slices of all segments of K, one behind another; the loads run ahead.
+  const int per_segment = static_cast<int>((p.K + kDepth - 1) / kDepth);
+  const int slices = per_segment * p.segments;
+  int ahead = 0;                     // next slice to load
+  int left = static_cast<int>(p.K);  // positions along k from it to its segment's end
+  auto advance = [&] {
+    ++ahead;
+    left -= kDepth;
+    oa.advance();
+    ob.advance();
+    if (ahead == per_segment && p.segments == 2) {
+      left = static_cast<int>(p.K);
+      oa.p = static_cast<const T*>(p.a[1]) + m0 * p.sam;
+      ob.p = static_cast<const T*>(p.b[1]) + n0 * p.sbn;
+    }
+  };
+  auto multiply = [&](int slot) {
+#pragma unroll
+    for (int d = 0; d < kDepth / kGroups<BT>; ++d) {
+      const int k = group * (kDepth / kGroups<BT>) + d;
+      float x[R];
+      uint64_t w[R / 2];
+#pragma unroll
+      for (int h = 0; h < R / 4; ++h)
+        *reinterpret_cast<float4*>(&x[4 * h]) = *reinterpret_cast<const float4*>(&sa[slot][k][ty * 4 + h * STEP]);
+#pragma unroll
+      for (int h = 0; h < R / 4; ++h) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sb[slot][k][tx * 4 + h * STEP]);
+        w[2 * h] = two.x;
+        w[2 * h + 1] = two.y;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint64_t xx = twice(x[i]);
+#pragma unroll
+        for (int j = 0; j < R / 2; ++j) fma2(acc2[i][j], xx, w[j]);
+      }
+    }
+  };
+  if constexpr (kAsync) {
+    auto issue = [&] {  // (a group each time, an empty one at the end)
+      if (ahead < slices) {
+        slice_async<BT>(oa, left, sa[ahead % RING]);
+        slice_async<BT>(ob, left, sb[ahead % RING]);
+        advance();
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < RING - 1; ++i) issue();
+    for (int s = 0; s < slices; ++s) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
+      __syncthreads();  // slice s is there for all; all are done with slice s - 1, whose slot the next load takes
+      issue();
+      multiply(s % RING);
+    }
+  } else {
+    float va[kShare<BT>], vb[kShare<BT>];
+    auto fetch = [&] {
+      slice_load<BT>(oa, left, va);
+      slice_load<BT>(ob, left, vb);
+      advance();
+    };
+    fetch();
+    for (int s = 0; s < slices; ++s) {
+      slice_store<BT>(p.sak == 1, va, sa[s % RING]);
+      slice_store<BT>(p.sbk == 1, vb, sb[s % RING]);
+      __syncthreads();  // (this slot's last readers are past an earlier barrier)
+      if (ahead < slices) fetch();
+      multiply(s % RING);
+    }
+  }
 
   float acc[R][R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
-
-  Slice<T, BT> la, lb;
-  int buf = 0;
-  for (int seg = 0; seg < p.segments; ++seg) {
-    const T* A = static_cast<const T*>(p.a[seg]);
-    const T* B = static_cast<const T*>(p.b[seg]);
-    const T* B2 = static_cast<const T*>(p.b[1]);  // up: Wu
-    const bool ak = p.sak == 1, bk = p.sbk == 1;
-    auto fetch = [&](long long k0) {
-      la.load(A, p.sam, p.sak, m0, p.M, k0, p.K, 0, 0);
-      if (MODE == FFN_UP) {
-        lb.load(B, p.sbn, p.sbk, n0, p.N, k0, p.K, 0, BN);
-        lb.load(B2, p.sbn, p.sbk, n0, p.N, k0, p.K, BN, BN);
-      } else {
-        lb.load(B, p.sbn, p.sbk, n0, p.N, k0, p.K, 0, 0);
-      }
+    for (int j = 0; j < R / 2; ++j)
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(acc2[i][j]));
+  if constexpr (kGroups<BT> == 4) {
+    // The four groups' sums join in shared memory, (0 + 2) + (1 + 3), each
+    // thread's 64 values a lane's distance apart.
+    constexpr int kLanes = kSimtThreads / 4;
+    float* own = &sa[0][0][0] + threadIdx.x % kLanes;
+    float* odd = &sb[0][0][0] + threadIdx.x % kLanes;
+    auto put_sums = [&](float* to) {
+#pragma unroll
+      for (int i = 0; i < R * R; ++i) to[i * kLanes] = acc[i / R][i % R];
     };
-    fetch(0);
-    for (long long k0 = 0; k0 < p.K; k0 += kDepth) {
-      la.store(sa[buf], ak);
-      lb.store(sb[buf], bk);
-      __syncthreads();  // (the other buffer's readers are past the barrier before this one)
-      if (k0 + kDepth < p.K) fetch(k0 + kDepth);
+    auto add_sums = [&](const float* from) {
 #pragma unroll
-      for (int k = 0; k < kDepth; ++k) {
-        float x[R], w[R];
+      for (int i = 0; i < R * R; ++i) acc[i / R][i % R] += from[i * kLanes];
+    };
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if (group == 2) put_sums(own);
+    if (group == 3) put_sums(odd);
+    __syncthreads();
+    if (group == 0) add_sums(own);
+    if (group == 1) add_sums(odd);
+    __syncthreads();
+    if (group == 1) put_sums(own);
+    __syncthreads();
+    // The tile, row by row, for all 256 threads to finish.
+    float(*whole)[BT] = reinterpret_cast<float(*)[BT]>(&sb[0][0][0]);
+    if (group == 0) {
+      add_sums(own);
 #pragma unroll
-        for (int h = 0; h < R / 4; ++h)
-          *reinterpret_cast<float4*>(&x[4 * h]) = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 4 + h * STEP]);
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int h = 0; h < R / CW; ++h) {
-          if (CW == 4)
-            *reinterpret_cast<float4*>(&w[CW * h]) =
-                *reinterpret_cast<const float4*>(&sb[buf][k][tx * CW + h * CSTEP]);
-          else
-            *reinterpret_cast<float2*>(&w[CW * h]) =
-                *reinterpret_cast<const float2*>(&sb[buf][k][tx * CW + h * CSTEP]);
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int j = 0; j < R; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
-      }
-      buf ^= 1;
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float4*>(&whole[ty * 4 + (i / 4) * STEP + i % 4][tx * 4 + h * STEP]) =
+              *reinterpret_cast<const float4*>(&acc[i][4 * h]);
     }
-  }
-
+    __syncthreads();
+#pragma unroll 4
+    for (int e = threadIdx.x; e < BT * BN; e += kSimtThreads) {
+      const int r = e / BN, c = e % BN;
+      if (m0 + r < p.M && n0 + c < p.N) finish<T, MODE>(a, p, m0 + r, n0 + c, whole[r][c], whole[r][(c + BN) % BT]);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const long long m = m0 + ty * 4 + (i / 4) * STEP + i % 4;
-    if (m >= p.M) continue;
-    if (MODE == FFN_UP) {
-      // a thread's first group of columns are gates, its second the ups of the same elements
+    for (int i = 0; i < R; ++i) {
+      const long long m = m0 + ty * 4 + (i / 4) * STEP + i % 4;
+      if (m >= p.M) continue;
 #pragma unroll
-      for (int j = 0; j < CW; ++j) {
-        const long long n = n0 + tx * CW + j;
-        if (n >= p.N) continue;
-        const long long at = m * p.N + n;
-        const float g = acc[i][j], u = acc[i][j + CW];
-        float slope;
-        put(static_cast<T*>(p.c) + at, act_of(a.act, g, &slope) * u);
-        if (a.saved != nullptr) {
-          const long long sv = ffn_saved_at(m, n, p.N);
-          a.saved[sv] = g;
-          a.saved[ffn_saved_plane(p.M, p.N) + sv] = u;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const long long n = n0 + tx * CW + (j / CW) * CSTEP + j % CW;
-        if (n >= p.N) continue;
-        const long long at = m * p.N + n;
-        if (MODE == FFN_DGATE) {
-          const long long sv = ffn_saved_at(m, n, p.N);
-          const float g = a.saved[sv], u = a.saved[ffn_saved_plane(p.M, p.N) + sv], da = acc[i][j];
-          float slope;
-          const float h = act_of(a.act, g, &slope);
-          const long long one = p.M * p.N;
-          put(static_cast<T*>(p.c) + at, h * u);               // a
-          put(static_cast<T*>(p.c) + one + at, da * u * slope);  // dg
-          put(static_cast<T*>(p.c) + 2 * one + at, da * h);      // du
-        } else {
-          put(static_cast<T*>(p.c) + at, acc[i][j]);
-        }
+      for (int j = 0; j < (MODE == FFN_UP ? 4 : R); ++j) {
+        // up: a thread's first group of columns are gates, its second the ups of the same elements
+        const long long n = n0 + tx * 4 + (j / 4) * STEP + j % 4;
+        if (n < p.N) finish<T, MODE>(a, p, m, n, acc[i][j], acc[i][(j + 4) % R]);
       }
     }
   }
@@ -215,8 +360,10 @@ static cudaError_t launch_simt_bt(int mode, FfnSimtArgs& a, cudaStream_t s) {
 cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s) {
   long long big = 0;
   for (int i = 0; i < a.n; ++i) big += (a.p[i].M + 127) / 128 * ((a.p[i].N + (mode == FFN_UP ? 63 : 127)) / (mode == FFN_UP ? 64 : 128));
-  // 128-wide tiles do twice the work for each shared load; below one tile an SM the 64-wide ones use more SMs
-  const bool wide = big >= sms;
+  // 128-wide tiles do twice the work for each shared load, but take four times
+  // as long each, one or two on an SM: they pay from some two waves on (T = 2000, H = O = 1024,
+  // F = 2048: 2.06 ms forward and backward against 2.35).
+  const bool wide = big >= 2 * sms;
   if (bf16)
     return wide ? launch_simt_bt<__nv_bfloat16, 128>(mode, a, s) : launch_simt_bt<__nv_bfloat16, 64>(mode, a, s);
   return wide ? launch_simt_bt<float, 128>(mode, a, s) : launch_simt_bt<float, 64>(mode, a, s);

@@ -8,41 +8,52 @@ single passes.  Everything runs in the CUDA library on the current stream."""
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import RKLError, _check, _dtype_code, _ptr, _stream, lib
+from .binding import DT_BF16, DT_FP32, RKLError, _check, _on_device, _raw_stream, lib
 
 ACT_SILU = 0
 ACT_GELU = 1
 ACT_GELU_TANH = 2
 ACT_RELU = 3
 
+_CODES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
+
 
 def _sizes(x, W_gate, W_up, W_down):
-    """(T, H, F, O) of a block, checked."""
-    for name, t in (("x", x), ("W_gate", W_gate), ("W_up", W_up), ("W_down", W_down)):
-        if not t.is_cuda or t.device != x.device or t.layout != torch.strided:
-            raise RKLError(2, "%s must be a dense CUDA tensor beside x" % name)
-        if t.dtype != x.dtype:
-            raise RKLError(3, "%s is %s, x is %s" % (name, t.dtype, x.dtype))
-    _dtype_code(x)
-    if x.dim() != 2 or W_gate.dim() != 2 or W_up.shape != W_gate.shape or W_down.dim() != 2:
+    """(dtype code, T, H, F, O) of a block, checked."""
+    dtype, index = x.dtype, x.get_device()
+    if not (W_gate.dtype == W_up.dtype == W_down.dtype == dtype and x.is_cuda and
+            W_gate.get_device() == W_up.get_device() == W_down.get_device() == index):
+        for name, t in (("x", x), ("W_gate", W_gate), ("W_up", W_up), ("W_down", W_down)):
+            if not t.is_cuda or t.get_device() != index:
+                raise RKLError(2, "%s must be a CUDA tensor on the device of x" % name)
+            if t.dtype != dtype:
+                raise RKLError(3, "%s is %s, x is %s" % (name, t.dtype, dtype))
+    code = _CODES.get(dtype)
+    if code is None:
+        raise RKLError(3, "unsupported dtype %s" % (dtype,))
+    shape = W_gate.shape
+    if x.dim() != 2 or len(shape) != 2 or W_up.shape != shape or W_down.dim() != 2:
         raise RKLError(2, "x [T, H], W_gate and W_up [F, H], W_down [O, F] expected")
-    (T, H), (F, H2), (O, F2) = x.shape, W_gate.shape, W_down.shape
+    (T, H), (F, H2), (O, F2) = x.shape, shape, W_down.shape
     if H != H2 or F != F2:
-        raise RKLError(2, "sizes do not fit: x %s, W_gate %s, W_down %s" % (tuple(x.shape), tuple(W_gate.shape),
+        raise RKLError(2, "sizes do not fit: x %s, W_gate %s, W_down %s" % (tuple(x.shape), tuple(shape),
                                                                             tuple(W_down.shape)))
-    return T, H, F, O
+    return code, T, H, F, O
 
 
-def _workspace(x, T, H, F, O, backward):
+@lru_cache(maxsize=1024)
+def _workspace_size(code, T, H, F, O, backward):
     nbytes = ctypes.c_size_t(0)
-    _check(lib().rkl_ffn_workspace_size(_dtype_code(x), T, H, F, O, backward, ctypes.byref(nbytes)))
-    return torch.empty(nbytes.value, dtype=torch.uint8, device=x.device)
+    _check(lib().rkl_ffn_workspace_size(code, T, H, F, O, backward, ctypes.byref(nbytes)))
+    return nbytes.value
 
 
+@lru_cache(maxsize=1024)
 def _saved_size(T, F):
     n = ctypes.c_int64(0)
     _check(lib().rkl_ffn_saved_size(T, F, ctypes.byref(n)))
@@ -52,32 +63,41 @@ def _saved_size(T, F):
 def ffn_forward(x, W_gate, W_up, W_down, activation=ACT_SILU, save=False):
     """(y [T, O], saved): saved (fp32, g and u in the library's own order, for
     ``ffn_backward``) is None unless ``save``."""
-    T, H, F, O = _sizes(x, W_gate, W_up, W_down)
-    x, W_gate, W_up, W_down = (t.contiguous() for t in (x, W_gate, W_up, W_down))
-    with torch.cuda.device(x.device):
-        y = torch.empty((T, O), dtype=x.dtype, device=x.device)
-        saved = torch.empty(_saved_size(T, F), dtype=torch.float32, device=x.device) if save else None
-        ws = _workspace(x, T, H, F, O, 0)
-        _check(lib().rkl_ffn_forward(_ptr(x), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _dtype_code(x), activation,
-                                     T, H, F, O, _ptr(y), _ptr(saved), _ptr(ws), ws.numel(), _stream(x.device)))
+    code, T, H, F, O = _sizes(x, W_gate, W_up, W_down)
+    # (bound to names: a copy has to live until the call returns)
+    x, W_gate, W_up, W_down = x.contiguous(), W_gate.contiguous(), W_up.contiguous(), W_down.contiguous()
+    device = x.device
+    with _on_device(device.index):
+        y = torch.empty((T, O), dtype=x.dtype, device=device)
+        saved = torch.empty(_saved_size(T, F), dtype=torch.float32, device=device) if save else None
+        nbytes = _workspace_size(code, T, H, F, O, 0)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _check(lib().rkl_ffn_forward(x.data_ptr(), W_gate.data_ptr(), W_up.data_ptr(), W_down.data_ptr(), code, activation,
+                                     T, H, F, O, y.data_ptr(), saved.data_ptr() if save else None, ws.data_ptr(), nbytes,
+                                     _raw_stream(device.index)))
     return y, saved
 
 
 def ffn_backward(x, W_gate, W_up, W_down, dy, saved, activation=ACT_SILU, needs=(True, True, True, True)):
     """(dx, dW_gate, dW_up, dW_down) in the dtype of x; None where ``needs``
     says so."""
-    T, H, F, O = _sizes(x, W_gate, W_up, W_down)
-    if dy.shape != (T, O) or dy.device != x.device or dy.dtype != x.dtype:
+    code, T, H, F, O = _sizes(x, W_gate, W_up, W_down)
+    device = x.device
+    if dy.shape != (T, O) or dy.device != device or dy.dtype != x.dtype:
         raise RKLError(2, "dy must be a [%d, %d] tensor of x's dtype and device" % (T, O))
-    if saved.shape != (_saved_size(T, F),) or saved.dtype != torch.float32 or saved.device != x.device or not saved.is_contiguous():
+    if saved.shape != (_saved_size(T, F),) or saved.dtype != torch.float32 or saved.device != device \
+            or not saved.is_contiguous():
         raise RKLError(2, "saved must be what ffn_forward gave for the same sizes")
-    x, W_gate, W_up, W_down, dy = (t.contiguous() for t in (x, W_gate, W_up, W_down, dy))
-    with torch.cuda.device(x.device):
+    x, W_gate, W_up, W_down = x.contiguous(), W_gate.contiguous(), W_up.contiguous(), W_down.contiguous()
+    dy = dy.contiguous()
+    with _on_device(device.index):
         out = [torch.empty_like(t) if need else None for t, need in zip((x, W_gate, W_up, W_down), needs)]
-        ws = _workspace(x, T, H, F, O, 1)
-        _check(lib().rkl_ffn_backward(_ptr(x), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _dtype_code(x), activation,
-                                      T, H, F, O, _ptr(dy), _ptr(saved), *[_ptr(t) for t in out], _ptr(ws), ws.numel(),
-                                      _stream(x.device)))
+        nbytes = _workspace_size(code, T, H, F, O, 1)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _check(lib().rkl_ffn_backward(x.data_ptr(), W_gate.data_ptr(), W_up.data_ptr(), W_down.data_ptr(), code, activation,
+                                      T, H, F, O, dy.data_ptr(), saved.data_ptr(),
+                                      *[None if t is None else t.data_ptr() for t in out], ws.data_ptr(), nbytes,
+                                      _raw_stream(device.index)))
     return tuple(out)
 
 

@@ -13,10 +13,12 @@ replays count the steps themselves.
 from __future__ import annotations
 
 import ctypes
+from array import array
+from functools import lru_cache
 
 import torch
 
-from .binding import DT_BF16, DT_FP32, RKLError, _check, _ptr, _stream, lib
+from .binding import DT_BF16, DT_FP32, RKLError, _check, _on_device, _raw_stream, lib
 
 _CODES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
 STATE_BLOCK = 256  # elements under one scale of an 8-bit state; each tensor's place in the state is a multiple
@@ -29,18 +31,38 @@ def _code(t, what):
     return c
 
 
-def _norm_into(grads, device):
-    """The launches of grad_norm over contiguous gradients on `device`."""
-    n = len(grads)
+def _address(a):
+    """Of the entries of an `array` (which the caller keeps)."""
+    return a.buffer_info()[0]
+
+
+@lru_cache(maxsize=64)
+def _norm_workspace_size(n):
     nbytes = ctypes.c_size_t(0)
     _check(lib().rkl_grad_norm_workspace_size(n, ctypes.byref(nbytes)))
-    ws = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    return nbytes.value
+
+
+def _norm_into(n, ptrs, numel, codes, device):
+    """The launches of grad_norm over n contiguous gradients on the current
+    device, given as arrays of addresses (0: absent), element counts and dtype
+    codes."""
+    nbytes = _norm_workspace_size(n)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     norm = torch.empty(1, dtype=torch.float32, device=device)
-    _check(lib().rkl_grad_norm(n, (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]),
-                               (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
-                               (ctypes.c_int32 * n)(*[_code(g, "a gradient") for g in grads]),
-                               _ptr(norm), _ptr(ws), nbytes.value, _stream(device)))
+    _check(lib().rkl_grad_norm(n, _address(ptrs), _address(numel), _address(codes), norm.data_ptr(), ws.data_ptr(), nbytes,
+                               _raw_stream(device.index)))
     return norm
+
+
+def _dtype_codes(tensors, what):
+    """Their dtype codes as an array (of a ``None``: fp32's)."""
+    try:
+        return array("i", [DT_FP32 if t is None else _CODES[t.dtype] for t in tensors])
+    except KeyError:
+        for i, t in enumerate(tensors):
+            _code(t, "%s %d" % (what, i))
+        raise
 
 
 def grad_norm(grads):
@@ -50,12 +72,15 @@ def grad_norm(grads):
     if not grads:
         raise RKLError(2, "grad_norm needs a gradient")
     device = grads[0].device
+    index = grads[0].get_device()
     for g in grads:
-        if not g.is_cuda or g.device != device or g.layout != torch.strided:
+        if not g.is_cuda or g.get_device() != index or g.is_sparse:
             raise RKLError(2, "gradients must be dense CUDA tensors on one device")
-        _code(g, "a gradient")
-    with torch.cuda.device(device):
-        return _norm_into([g if g.is_contiguous() else g.contiguous() for g in grads], device)
+    codes = _dtype_codes(grads, "gradient")
+    with _on_device(index):
+        grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
+        return _norm_into(len(grads), array("Q", [g.data_ptr() for g in grads]), array("q", [g.numel() for g in grads]), codes,
+                          device)
 
 
 class AdamW:
@@ -84,6 +109,8 @@ class AdamW:
         if n == 0:
             raise RKLError(2, "AdamW needs a parameter")
         device = self.params[0].device
+        if not self.params[0].is_cuda:
+            raise RKLError(2, "parameters must be CUDA tensors")
         for i, p in enumerate(self.params):
             if not p.is_cuda or p.device != device or p.layout != torch.strided or not p.is_contiguous():
                 raise RKLError(2, "parameter %d: parameters must be contiguous CUDA tensors on one device" % i)
@@ -103,9 +130,9 @@ class AdamW:
         self.lr, self.betas, self.eps = self._checked_lr(lr, device), tuple(betas), eps
         self.weight_decay, self.state_bits, self.seed, self.device = decay, state_bits, int(seed) & 0xFFFFFFFF, device
 
-        self._numel = (ctypes.c_int64 * n)(*[p.numel() for p in self.params])
-        offsets, total = (ctypes.c_int64 * n)(), ctypes.c_int64(0)
-        _check(lib().rkl_adamw_state_size(n, self._numel, offsets, ctypes.byref(total)))
+        self._numel = array("q", [p.numel() for p in self.params])
+        offsets, total = array("q", [0] * n), ctypes.c_int64(0)
+        _check(lib().rkl_adamw_state_size(n, _address(self._numel), _address(offsets), ctypes.byref(total)))
         self.offsets, total = list(offsets), total.value
         dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
         self.exp_avg = torch.zeros(total, dtype=torch.uint8 if state_bits == 8 else dt, device=device).view(dt)
@@ -122,9 +149,9 @@ class AdamW:
         self.steps = self._control[:1]
 
         self._shapes = [p.shape for p in self.params]
-        self._ptrs = (ctypes.c_void_p * n)(*[p.data_ptr() for p in self.params])
-        self._dtypes = (ctypes.c_int32 * n)(*[_CODES[p.dtype] for p in self.params])
-        self._decay = (ctypes.c_float * n)(*decay)
+        self._ptrs = array("Q", [p.data_ptr() for p in self.params])
+        self._dtypes = _dtype_codes(self.params, "parameter")
+        self._decay = array("f", decay)
         # an update moves a tensor's version, so that a backward pass through an older value is refused
         self._tracked = [p for p in self.params if not p.is_inference()]
 
@@ -145,9 +172,8 @@ class AdamW:
         With either, a step whose norm is infinite or NaN changes nothing and
         does not count.  Returns the norm (None without either)."""
         n, device = len(self.params), self.device
-        for i, p in enumerate(self.params):
-            if p.data_ptr() != self._ptrs[i] and p.numel():
-                raise RKLError(2, "parameter %d moved in memory since AdamW was made" % i)
+        if array("Q", [p.data_ptr() for p in self.params]) != self._ptrs:
+            raise RKLError(2, "a parameter moved in memory since AdamW was made")
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != n:
             raise RKLError(2, "%d gradients for %d parameters" % (len(grads), n))
@@ -156,28 +182,30 @@ class AdamW:
             raise RKLError(2, "max_norm = %r is not positive" % (max_norm,))
         if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != device):
             raise RKLError(2, "norm must be a 1-element float32 tensor beside the parameters")
-        codes = []
-        for i, g in enumerate(grads):
-            if g is None:
-                codes.append(DT_FP32)
-                continue
-            if g.shape != self._shapes[i] or g.device != device or g.layout != torch.strided:
-                raise RKLError(2, "gradient %d must be a dense tensor of its parameter's shape and device" % i)
-            codes.append(_code(g, "gradient %d" % i))
-            if not g.is_contiguous():
-                grads[i] = g.contiguous()
-        with torch.cuda.device(device):
+        index = device.index
+        ptrs = array("Q", bytes(8 * n))
+        with _on_device(index):
+            for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+                if g is None:
+                    continue
+                if g.shape != shape or g.get_device() != index or g.is_sparse:
+                    raise RKLError(2, "gradient %d must be a dense tensor of its parameter's shape and device" % i)
+                if not g.is_contiguous():
+                    g = grads[i] = g.contiguous()
+                ptrs[i] = g.data_ptr()
+            codes = _dtype_codes(grads, "gradient")
             if max_norm is not None and norm is None:
-                present = [g for g in grads if g is not None]
-                norm = _norm_into(present, device) if present else torch.zeros(1, device=device)
+                norm = _norm_into(n, ptrs, self._numel, codes, device)
             lr_dev = lr if isinstance(lr, torch.Tensor) else None
+            small = self.state_bits == 8
             _check(lib().rkl_adamw_step(
-                n, self._ptrs, (ctypes.c_void_p * n)(*[None if g is None else g.data_ptr() for g in grads]),
-                self._numel, self._dtypes, (ctypes.c_int32 * n)(*codes), self._decay, self.state_bits,
-                _ptr(self.exp_avg), _ptr(self.exp_avg_sq), _ptr(self.exp_avg_scale), _ptr(self.exp_avg_sq_scale),
-                _ptr(self.master), _ptr(self._control), 0.0 if lr_dev is not None else float(lr), _ptr(lr_dev),
-                self.betas[0], self.betas[1], self.eps, self.seed, _ptr(norm),
-                float("inf") if max_norm is None else float(max_norm), _stream(device)))
+                n, _address(self._ptrs), _address(ptrs), _address(self._numel), _address(self._dtypes), _address(codes),
+                _address(self._decay), self.state_bits, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
+                self.exp_avg_scale.data_ptr() if small else None, self.exp_avg_sq_scale.data_ptr() if small else None,
+                None if self.master is None else self.master.data_ptr(), self._control.data_ptr(),
+                0.0 if lr_dev is not None else float(lr), None if lr_dev is None else lr_dev.data_ptr(),
+                self.betas[0], self.betas[1], self.eps, self.seed, None if norm is None else norm.data_ptr(),
+                float("inf") if max_norm is None else float(max_norm), _raw_stream(index)))
         if self._tracked:
             torch.autograd.graph.increment_version(self._tracked)
         return norm
