@@ -1244,7 +1244,7 @@ rkl_status rkl_adamw_step(int32_t n, void* const* params, const void* const* gra
       // (a step with nothing to update still counts)
       a.advance = i == n;
       const int64_t need = (a.blocks + kOptWarps - 1) / kOptWarps;
-      const int64_t most = int64_t(sms) * kOptGridPerSm;
+      const int64_t most = int64_t(sms) * (state_bits == 8 ? kOpt8PerSm : kOptPerSm);
       RKL_CUDA(launch_adamw(state_bits, a, static_cast<int>(need < 1 ? 1 : (need < most ? need : most)),
                             static_cast<cudaStream_t>(stream)));
       a.n = 0;
@@ -1311,7 +1311,7 @@ rkl_status rkl_grad_norm(int32_t n, const void* const* grads, const int64_t* num
     if (a.n > 0 && (i == n || (taken && (a.n == kOptTensors || chunks + more > INT32_MAX / 2)))) {
       a.chunks = static_cast<int>(chunks);
       const int64_t need = (chunks + kOptWarps - 1) / kOptWarps;
-      const int most = sms * 8 < kNormMaxGrid ? sms * 8 : kNormMaxGrid;
+      const int most = sms * kNormPerSm < kNormMaxGrid ? sms * kNormPerSm : kNormMaxGrid;
       const int grid = static_cast<int>(need < most ? need : most);
       if ((partials + grid) * sizeof(double) > workspace_bytes)
         return fail(RKL_ERR_SHAPE, "the gradients have too many elements for %d tensors", n);
@@ -1486,7 +1486,7 @@ static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bo
 }
 
 static rkl_status skinny_product(const SkinnyPlan& p, const void* x, const void* W1, int64_t R1, const void* W2, int64_t T,
-                                 int64_t K, float* part, cudaStream_t s) {
+                                 int64_t K, float* part, bool follows, cudaStream_t s) {
   FfnSkinnyArgs a = {};
   a.cols = static_cast<int>((T + 15) / 16 * 16);
   RKL_TRY(operand_map(&a.w1, W1, R1, K, false));
@@ -1500,6 +1500,7 @@ static rkl_status skinny_product(const SkinnyPlan& p, const void* x, const void*
   a.T = static_cast<int>(T);
   a.pitch = p.pitch;
   a.parts = p.parts;
+  a.follows = follows;
   RKL_CUDA(launch_ffn_skinny(a, p.grid, s));
   return RKL_OK;
 }
@@ -1540,9 +1541,9 @@ static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_
                                  float* saved, uint8_t* ws, int sms, cudaStream_t s) {
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   if (p.skinny) {
-    RKL_TRY(skinny_product(p.up, x, W_gate, F, W_up, T, H, part, s));
+    RKL_TRY(skinny_product(p.up, x, W_gate, F, W_up, T, H, part, false, s));
     RKL_TRY(join_skinny(p.up, act, part, ws, saved, T, F, s));
-    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, T, F, part, s));
+    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, T, F, part, true, s));
     return join_skinny(p.down, -1, part, y, nullptr, T, O, s);
   }
   FfnPairArgs a = {};
@@ -1550,6 +1551,7 @@ static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_
   a.saved = saved;
   RKL_CUDA(launch_ffn_pair(FFN_UP, act, a, sms, s));
   FfnPairArgs d = {};
+  d.follows = true;
   RKL_TRY(pair_product(d, ws, nullptr, false, W_down, nullptr, false, p.parts > 1 ? static_cast<void*>(part) : y, T, O, F,
                        false, p.parts, p.part_rows));
   RKL_CUDA(launch_ffn_pair(FFN_GEMM, act, d, sms, s));
@@ -1572,6 +1574,7 @@ static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W
   RKL_CUDA(launch_ffn_pair(FFN_DGATE, act, a, sms, s));
   // longest items (K = 2 F) first
   FfnPairArgs d = {};
+  d.follows = true;
   d.counter = counter;
   if (dx)
     RKL_TRY(pair_product(d, dg, du, false, W_gate, W_up, true, p.parts > 1 ? static_cast<void*>(part) : dx, T, H, F, false,

@@ -16,6 +16,25 @@ __device__ __forceinline__ float act_sigmoid(float x) {
   return 1.f / (1.f + expf(-x));
 }
 
+// erfc(z) / 2 for z >= 0 by the Chebyshev fit t exp(-z^2 + P(t)), t = 1 / (1 +
+// z / 2), of Press, Teukolsky, Vetterling and Flannery, "Numerical Recipes"
+// (relative error 1.2e-7 for all z): about 16 instructions, a third of erfcf's.
+__device__ __forceinline__ float half_erfc_fit(float z) {
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, z, 1.f)));
+  float p = 0.17087277f;
+  p = fmaf(p, t, -0.82215223f);
+  p = fmaf(p, t, 1.48851587f);
+  p = fmaf(p, t, -1.13520398f);
+  p = fmaf(p, t, 0.27886807f);
+  p = fmaf(p, t, -0.18628806f);
+  p = fmaf(p, t, 0.09678418f);
+  p = fmaf(p, t, 0.37409196f);
+  p = fmaf(p, t, 1.00002368f);
+  p = fmaf(p, t, -1.26551223f);
+  return 0.5f * t * __expf(fmaf(-z, z, p));
+}
+
 // act(g), and in *slope its derivative.
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_with_slope(float g, float* slope) {
@@ -26,7 +45,13 @@ __device__ __forceinline__ float act_with_slope(float g, float* slope) {
   }
   if (ACT == ACT_GELU) {
     // g Phi(g), Phi = erfc(-g / sqrt(2)) / 2: no cancellation for negative g
-    const float phi = 0.5f * erfcf(-0.7071067811865476f * g);
+    float phi;
+    if (FAST) {
+      const float tail = half_erfc_fit(0.7071067811865476f * fabsf(g));  // Phi(-|g|)
+      phi = g < 0.f ? tail : 1.f - tail;
+    } else {
+      phi = 0.5f * erfcf(-0.7071067811865476f * g);
+    }
     const float e = FAST ? __expf(-0.5f * g * g) : expf(-0.5f * g * g);
     *slope = fmaf(g, 0.3989422804014327f * e, phi);
     return g * phi;

@@ -183,6 +183,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  if (threadIdx.x == 0) let_next_launch_begin();
+  wait_for_last_launch();
   // the next launch of this call counts its tiles from zero
   if (a.zero_counter != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.zero_counter = 0;
 
@@ -521,26 +523,47 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  if (threadIdx.x == 0) let_next_launch_begin();
 
   if (warp == 0) {
     if (lane == 0) {
+      // The weights do not depend on the launch before this one, x and the
+      // parts' memory may: the ring fills with weights first, up to 216 KB on
+      // each SM while that launch ends.
+      auto load_w = [&](int st, int tile, int k) {
+        const bool second = tile >= a.tiles_first;
+        mbar_arrive_expect_tx(&full[st], stage_bytes);
+        tma_load_2d(smem + st * stage_bytes, second ? &a.w2 : &a.w1, &full[st], k * kBK,
+                    (second ? tile - a.tiles_first : tile) * 128);
+      };
+      auto load_x = [&](int st, int k) {
+        tma_load_2d(smem + st * stage_bytes + kOperand, &a.x, &full[st], k * kBK, 0);
+      };
       int stage = 0;
       uint32_t phase = 0, armed = 0, last_par = 0;
       int tile = static_cast<int>(lo / a.steps), k = static_cast<int>(lo % a.steps);
-      for (long long s = lo; s < hi; ++s) {
-        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
-          give_up(abort_flag, ERR_WAIT_TMA_EMPTY);
-          break;
+      const int early = hi - lo < a.stages ? static_cast<int>(hi - lo) : a.stages;
+      for (int i = 0, t = tile, kk = k; i < early; ++i) {
+        load_w(i, t, kk);
+        if (++kk == a.steps) {
+          kk = 0;
+          ++t;
         }
-        uint8_t* sa = smem + stage * stage_bytes;
-        const bool second = tile >= a.tiles_first;
+      }
+      wait_for_last_launch();
+      for (long long s = lo; s < hi; ++s) {
         if (!RKL_BOUNDS(tile < a.tiles && k < a.steps)) {
           give_up(abort_flag, ERR_BOUNDS);
           break;
         }
-        mbar_arrive_expect_tx(&full[stage], stage_bytes);
-        tma_load_2d(sa, second ? &a.w2 : &a.w1, &full[stage], k * kBK, (second ? tile - a.tiles_first : tile) * 128);
-        tma_load_2d(sa + kOperand, &a.x, &full[stage], k * kBK, 0);
+        if (s - lo >= early) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+            give_up(abort_flag, ERR_WAIT_TMA_EMPTY);
+            break;
+          }
+          load_w(stage, tile, k);
+        }
+        load_x(stage, k);
         armed |= 1u << stage;
         last_par = (last_par & ~(1u << stage)) | (phase << stage);
         if (++stage == a.stages) {
@@ -603,6 +626,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
       if (!mbar_wait(tear, 0, &never)) atomicOr(&g_ffn_err, ERR_WAIT_TEARDOWN);
     }
   } else {
+    wait_for_last_launch();
     const int quarter = warp & 3;
     int i = 0;
     for (long long s = lo; s < hi; ++i) {
@@ -675,6 +699,8 @@ __device__ __forceinline__ float4 sum_parts(const FfnJoinArgs& a, long long row,
 // n and u at a.second + n.
 template <bool GATED, int ACT>
 __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ FfnJoinArgs a) {
+  if (threadIdx.x == 0) let_next_launch_begin();
+  wait_for_last_launch();
   const int n4 = a.N / 4;  // N is a multiple of 8
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= static_cast<long long>(a.T) * n4) return;
@@ -722,38 +748,46 @@ cudaError_t ffn_tc_setup() {
   return allow_smem(ffn_skinny_kernel, kSkinnySmem);
 }
 
-template <typename K>
-static cudaError_t launch_ffn_pair_as(K kernel, int grid, cudaStream_t s, const FfnPairArgs& a) {
+// follows: the launch comes right behind another of the same call and may begin
+// while that one ends.
+template <typename K, typename A>
+static cudaError_t launch_ffn(K kernel, unsigned grid, unsigned threads, size_t smem, bool pairs, bool follows,
+                              cudaStream_t s, const A& a) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid & ~1);  // whole CTA pairs
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  if (pairs) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = 2;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  if (follows) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_ffn_pair(int mode, int act, const FfnPairArgs& a, int sms, cudaStream_t s) {
   LaunchScope scope(mode == FFN_UP ? K_FFN_UP_TC : mode == FFN_DGATE ? K_FFN_DGATE_TC : K_FFN_GEMM_TC, s);
-  const int grid = 2 * a.items < sms ? 2 * a.items : sms;
-  if (mode == FFN_GEMM) return launch_ffn_pair_as(ffn_pair_kernel<FFN_GEMM, 0>, grid, s, a);
+  const int grid = (2 * a.items < sms ? 2 * a.items : sms) & ~1;  // whole CTA pairs
+  if (mode == FFN_GEMM) return launch_ffn(ffn_pair_kernel<FFN_GEMM, 0>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
   if (mode == FFN_UP) switch (act) {
-      case ACT_SILU: return launch_ffn_pair_as(ffn_pair_kernel<FFN_UP, ACT_SILU>, grid, s, a);
-      case ACT_GELU: return launch_ffn_pair_as(ffn_pair_kernel<FFN_UP, ACT_GELU>, grid, s, a);
-      case ACT_GELU_TANH: return launch_ffn_pair_as(ffn_pair_kernel<FFN_UP, ACT_GELU_TANH>, grid, s, a);
-      default: return launch_ffn_pair_as(ffn_pair_kernel<FFN_UP, ACT_RELU>, grid, s, a);
+      case ACT_SILU: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_SILU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+      case ACT_GELU: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_GELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+      case ACT_GELU_TANH: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_GELU_TANH>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+      default: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_RELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
     }
   switch (act) {
-    case ACT_SILU: return launch_ffn_pair_as(ffn_pair_kernel<FFN_DGATE, ACT_SILU>, grid, s, a);
-    case ACT_GELU: return launch_ffn_pair_as(ffn_pair_kernel<FFN_DGATE, ACT_GELU>, grid, s, a);
-    case ACT_GELU_TANH: return launch_ffn_pair_as(ffn_pair_kernel<FFN_DGATE, ACT_GELU_TANH>, grid, s, a);
-    default: return launch_ffn_pair_as(ffn_pair_kernel<FFN_DGATE, ACT_RELU>, grid, s, a);
+    case ACT_SILU: return launch_ffn(ffn_pair_kernel<FFN_DGATE, ACT_SILU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+    case ACT_GELU: return launch_ffn(ffn_pair_kernel<FFN_DGATE, ACT_GELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+    case ACT_GELU_TANH: return launch_ffn(ffn_pair_kernel<FFN_DGATE, ACT_GELU_TANH>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+    default: return launch_ffn(ffn_pair_kernel<FFN_DGATE, ACT_RELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
   }
 }
 
@@ -761,22 +795,20 @@ cudaError_t launch_ffn_skinny(FfnSkinnyArgs a, int grid, cudaStream_t s) {
   LaunchScope scope(K_FFN_SKINNY_TC, s);
   const int stage = kOperand + a.cols * kBK * 2;
   a.stages = 221184 / stage < kSkinnyMaxStages ? 221184 / stage : kSkinnyMaxStages;
-  ffn_skinny_kernel<<<grid, kSkinnyThreads, kSkinnySmem, s>>>(a);
-  return cudaGetLastError();
+  return launch_ffn(ffn_skinny_kernel, grid, kSkinnyThreads, kSkinnySmem, false, a.follows, s, a);
 }
 
 cudaError_t launch_ffn_join(int act, const FfnJoinArgs& a, cudaStream_t s) {
   LaunchScope scope(K_FFN_JOIN, s);
   const long long blocks = (static_cast<long long>(a.T) * (a.N / 4) + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  const unsigned grid = static_cast<unsigned>(blocks);
   switch (act) {
-    case -1: ffn_join_kernel<false, 0><<<grid, 256, 0, s>>>(a); break;
-    case ACT_SILU: ffn_join_kernel<true, ACT_SILU><<<grid, 256, 0, s>>>(a); break;
-    case ACT_GELU: ffn_join_kernel<true, ACT_GELU><<<grid, 256, 0, s>>>(a); break;
-    case ACT_GELU_TANH: ffn_join_kernel<true, ACT_GELU_TANH><<<grid, 256, 0, s>>>(a); break;
-    default: ffn_join_kernel<true, ACT_RELU><<<grid, 256, 0, s>>>(a); break;
+    case -1: return launch_ffn(ffn_join_kernel<false, 0>, grid, 256, 0, false, true, s, a);
+    case ACT_SILU: return launch_ffn(ffn_join_kernel<true, ACT_SILU>, grid, 256, 0, false, true, s, a);
+    case ACT_GELU: return launch_ffn(ffn_join_kernel<true, ACT_GELU>, grid, 256, 0, false, true, s, a);
+    case ACT_GELU_TANH: return launch_ffn(ffn_join_kernel<true, ACT_GELU_TANH>, grid, 256, 0, false, true, s, a);
+    default: return launch_ffn(ffn_join_kernel<true, ACT_RELU>, grid, 256, 0, false, true, s, a);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t read_and_clear_ffn_error(int* code) {

@@ -272,10 +272,12 @@ cudaError_t launch_simt_gemm(const float* A, long long sam, long long sak, const
 // ---------------------------------------------------------------- optimizer step
 constexpr int kOptBlock = 256;     // elements of a state block (one scale of the 8-bit form, one warp's work)
 constexpr int kOptWarps = 8;       // warps of a block of the optimizer kernels
-constexpr int kOptGridPerSm = 8;   // blocks per SM of the optimizer kernels' largest grid
+// Blocks per SM of the largest grids: the norm runs in one wave, the steps in many
+// (blocks of 8-bit states take unequal time; 32-bit: 1.92 ms against 1.94 in one).
+constexpr int kOptPerSm = 16, kOpt8PerSm = 24, kNormPerSm = 5;
 constexpr int kNormChunk = 1024;   // elements a warp of the norm kernel takes at a time
 constexpr int kOptTensors = 400;   // tensors of one launch (their table travels in the kernel's parameters)
-constexpr int kNormMaxGrid = 1184;  // blocks (partial sums) of one norm launch: 8 on each of 148 SMs
+constexpr int kNormMaxGrid = 1184;  // most blocks (partial sums) of one norm launch
 enum : uint32_t {
   OPT_PARAM_BF16 = 1,
   OPT_GRAD_BF16 = 2,
@@ -374,6 +376,7 @@ struct FfnPairArgs {
   int* counter;            // claims work items (nullable: dealt out)
   int* zero_counter;       // set to 0 for the next launch (nullable)
   int n, items;
+  bool follows;            // right behind another launch of the same call
 };
 struct FfnSkinnyArgs {
   CUtensorMap w1, w2, x;   // weights, box {64, 128}; x, box {64, cols}
@@ -382,6 +385,7 @@ struct FfnSkinnyArgs {
   int tiles, tiles_first;  // 128-row tiles in all, and of w1
   int steps;               // 64-deep steps of a tile
   int T, cols, pitch, parts, stages;
+  bool follows;            // right behind another launch of the same call
 };
 struct FfnJoinArgs {
   const float* part;

@@ -129,7 +129,7 @@ constexpr float kTinyBlock = 7.888609e-31f;  // 2^-100: a block no larger than t
                                              // reciprocal would leave the range of fp32)
 constexpr float kLargeV = 16384.f;
 constexpr float kUlp = 5.9604645e-8f;        // 2^-24
-constexpr uint32_t kVNear = 24u << 4;        // fp32's error of v's place between two codes, in 2^-24 of the way
+constexpr uint32_t kVNear = 17u << 4;        // fp32's error of v's place between two codes, in 2^-24 of the way
 
 // The final mix of MurmurHash3 (Austin Appleby, public domain).
 __device__ __forceinline__ uint32_t mix32(uint32_t h) {
@@ -157,6 +157,35 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Two fp32 values in one register pair, one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(uint64_t p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // The four words' top bytes.
@@ -325,14 +354,16 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
 // bits, so the codes are always the formula's.  With u = 2^-24, r = value 448 /
 // largest:
 //   m: off by 5 u t, t = |b1 m| + |(1 - b1) g|, whatever cancels in it; the
-//      block's largest by as much of its own t, which is below largest +
-//      2 b1 448 scale; r by 5 u more: below t 448 / largest u (10 + 5 W), W that
-//      bound over the largest.
-//   v: all terms are positive: 24 u of r, a code's step is r / 16 at least.
-__global__ void __launch_bounds__(32 * kWarps, 4) adamw8_kernel(const __grid_constant__ AdamwArgs a) {
+//      block's largest by 5 u of its own t; r by 2 u more: below
+//      t 448 / largest u (7 + 5 W), W the block's largest t over the largest.
+//   v: all terms are positive, 7 u; the largest as much, r 2 u more: 16 u of r,
+//      and a code's step is r / 16 at least.
+__global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_constant__ AdamwArgs a) {
   __shared__ StepConsts k;
   begin_step(a, &k);
   if (k.skip) return;
+  const float step = k.step, root = k.root, clip = k.clip, lr = k.lr;
+  const uint32_t key = k.key;
   const int lane = threadIdx.x & 31;
   int t = -1, t_end = 0;
   for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < a.blocks; b += gridDim.x * kWarps) {
@@ -348,41 +379,64 @@ __global__ void __launch_bounds__(32 * kWarps, 4) adamw8_kernel(const __grid_con
     uint2* cm = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + s);
     uint2* cv = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + s);
     const uint2 om = __ldcs(cm), ov = __ldcs(cv);
+    // The next block's lines start on their way to L2: with 24 warps an SM the
+    // wait for memory showed otherwise.
+    const int ahead = gridDim.x * kWarps;
+    if (b + ahead < t_end) {
+      const long long far_on = static_cast<long long>(ahead) * kOptBlock;
+      prefetch_l2(cm + far_on / 8);
+      prefetch_l2(cv + far_on / 8);
+      prefetch_l2(static_cast<const char*>(x.grad) + (i + far_on) * (x.flags & OPT_GRAD_BF16 ? 2 : 4));
+      if (a.master != nullptr)
+        prefetch_l2(a.master + s + far_on);
+      else
+        prefetch_l2(static_cast<const char*>(x.param) + (i + far_on) * (x.flags & OPT_PARAM_BF16 ? 2 : 4));
+    }
     const float ms = a.m_scale[q], vs = a.v_scale[q];
-    float m[8], v[8], term[8];
-    float m_top = 0.f, v_top = 0.f;
+    uint64_t m[4], v[4], term[4];  // neighbouring elements in pairs
+    float m_top = 0.f, v_top = 0.f, term_top = 0.f;
     {
-      float g[8], p[8];
+      float g[8], p[8], mc[8], vc[8];
       load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i, x.n, g);
       float* master = a.master != nullptr ? a.master + s : nullptr;
       if (master != nullptr)
         ld8_f32(master, p);
       else
         load8(x.param, x.flags & OPT_PARAM_BF16, x.flags & OPT_WIDE_PARAM, i, x.n, p);
-      const float keep = 1.f - k.lr * x.decay;
-      const float mk = a.beta1 * ms, vk = a.beta2 * vs;
-      unpack_e4m3x8(om, m);
-      unpack_e4m3x8(ov, v);
+      unpack_e4m3x8(om, mc);
+      unpack_e4m3x8(ov, vc);
+      const float keep = 1.f - lr * x.decay, mk = a.beta1 * ms, vk = a.beta2 * vs;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float ge = g[e] * k.clip;
-        const float m1 = m[e] * mk, m2 = a.omb1 * ge;
-        m[e] = m1 + m2;
-        term[e] = fabsf(m1) + fabsf(m2);
-        v[e] = fmaf(a.omb2 * ge, ge, v[e] * vk);
-        p[e] = new_param(p[e], m[e], v[e], keep, k.step, k.root, a.eps);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        m_top = max3_nan(m_top, fabsf(m[e]), fabsf(m[e + 1]));
-        v_top = max3_nan(v_top, v[e], v[e + 1]);
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t ge = mul2(pair(g[2 * e], g[2 * e + 1]), pair(clip, clip));
+        const uint64_t m1 = mul2(pair(mc[2 * e], mc[2 * e + 1]), pair(mk, mk)), m2 = mul2(ge, pair(a.omb1, a.omb1));
+        m[e] = add2(m1, m2);
+        const float2 h1 = both(m1), h2 = both(m2), mf = both(m[e]);
+        const float t0 = fabsf(h1.x) + fabsf(h2.x), t1 = fabsf(h1.y) + fabsf(h2.y);
+        term[e] = pair(t0, t1);
+        v[e] = fma2(mul2(ge, pair(a.omb2, a.omb2)), ge, mul2(pair(vc[2 * e], vc[2 * e + 1]), pair(vk, vk)));
+        const float2 vf = both(v[e]);
+        // (as new_param does)
+        float q0, q1, r0, r1;
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(vf.x));
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(vf.y));
+        const float2 den = both(fma2(pair(q0, q1), pair(root, root), pair(a.eps, a.eps)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(den.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(den.y));
+        const uint64_t change = mul2(mul2(m[e], pair(-step, -step)), pair(r0, r1));
+        const float2 pf = both(fma2(pair(p[2 * e], p[2 * e + 1]), pair(keep, keep), change));
+        p[2 * e] = pf.x;
+        p[2 * e + 1] = pf.y;
+        m_top = max3_nan(m_top, fabsf(mf.x), fabsf(mf.y));
+        v_top = max3_nan(v_top, vf.x, vf.y);
+        term_top = max3_nan(term_top, t0, t1);
       }
       if (master != nullptr) st8_f32(master, p);
       store8(x.param, x.flags & OPT_PARAM_BF16, x.flags & OPT_WIDE_PARAM, i, x.n, p);
     }
-    const float mm = warp_max_magnitude(m_top), vm = warp_max_magnitude(v_top);
+    const float mm = warp_max_magnitude(m_top), vm = warp_max_magnitude(v_top), tm = warp_max_magnitude(term_top);
     const bool m_some = !(mm <= kTinyBlock), v_some = !(vm <= kTinyBlock);
-    const float mi = m_some ? __fdividef(kE4m3Max, mm) : 0.f, vi = v_some ? __fdividef(kE4m3Max, vm) : 0.f;
+    const float mi = m_some ? __fdiv_rn(kE4m3Max, mm) : 0.f, vi = v_some ? __fdiv_rn(kE4m3Max, vm) : 0.f;
     const bool far = vm > kLargeV;  // vi 2^-120 leaves fp32's normal range: all of v in 64 bits
     const float vi120 = vi * 7.52316384526264e-37f;
     const uint32_t least = v_some ? 0x01000000u : 0u;
@@ -390,42 +444,55 @@ __global__ void __launch_bounds__(32 * kWarps, 4) adamw8_kernel(const __grid_con
     // value, above the half step of the code.  Second moment stochastically:
     // with b2 = 0.999 a step moves it by less than half a code's step, and to
     // the nearest it would never move at all.
-    const float w = fmaf(896.f * a.beta1, ms, mm) * mi * (1.f / kE4m3Max);
-    const float off = mi * kUlp * fmaf(5.f, w, 10.f);
+    const float w = tm * mi * (1.f / kE4m3Max);
+    const float off = mi * kUlp * fmaf(5.f, w, 7.f);
     const uint32_t place =
-        static_cast<uint32_t>(s) ^ mix32(k.key + static_cast<uint32_t>(static_cast<unsigned long long>(s) >> 32));
-    // How much further |m| lies from the border next to it than fp32's error:
-    // half the code's step less the distance to the code.  The step is 2^-3 of
-    // 2^exponent (that of the smallest normal code at least); adding 2^20 times
-    // 2^exponent rounds to a multiple of it.
-    auto clear_of_border = [&](float me, float te) {
-      const float r = fabsf(me);
-      const float top = fmaxf(__uint_as_float(__float_as_uint(r) & 0x7f800000u), 0.015625f);
-      const float rest = r - (fmaf(top, 1048576.f, r) - top * 1048576.f);
-      return fmaf(te, -off, fmaf(top, 0.0625f, -fabsf(rest)));
+        static_cast<uint32_t>(s) ^ mix32(key + static_cast<uint32_t>(static_cast<unsigned long long>(s) >> 32));
+    // By how much two |m| lie in fp32's error of the border next to them (above
+    // 0: they do): distance to the code plus error less half the code's step.
+    // The step is 2^-3 of 2^exponent (that of the smallest normal code at least);
+    // adding 1.5 x 2^20 times 2^exponent rounds to a multiple of it.
+    auto in_reach = [&](uint64_t me, uint64_t te) {
+      const float2 r = both(me);
+      const uint64_t top = pair(fmaxf(__uint_as_float(__float_as_uint(r.x) & 0x7f800000u), 0.015625f),
+                                fmaxf(__uint_as_float(__float_as_uint(r.y) & 0x7f800000u), 0.015625f));
+      const uint64_t code = fma2(top, pair(-1572864.f, -1572864.f), fma2(top, pair(1572864.f, 1572864.f), me));
+      const float2 rest = both(fma2(code, pair(-1.f, -1.f), me));
+      const float2 room = both(fma2(te, pair(off, off), mul2(top, pair(-0.0625f, -0.0625f))));
+      return make_float2(fabsf(rest.x) + room.x, fabsf(rest.y) + room.y);
     };
     // r 2^-120 has e4m3's exponent and mantissa above 20 more bits; 16 times
     // them the code is the top byte, and adding 24 random bits (20 and 4 that
     // cannot matter) carries into it exactly when rest + random >= 1.
-    auto raised = [&](float ve, int e) {
+    auto raised = [&](float r120, int e) {
       const uint32_t h = mix32(place ^ static_cast<uint32_t>(e));
-      return __float_as_uint(ve * vi120) * 16u + (h >> 8);
+      return __float_as_uint(r120) * 16u + (h >> 8);
     };
     auto v_window = [](uint32_t y) { return y * 256u + (kVNear << 8); };  // below 2 kVNear << 8: next to a border
-    float nearest_m = 1.f;
+    float reach = -1.f;
     uint32_t nearest_v = 0xffffffffu, y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      m[e] *= mi;
-      nearest_m = fminf(nearest_m, clear_of_border(m[e], term[e]));
-      y[e] = raised(v[e], e);
-      nearest_v = min(nearest_v, v_window(y[e]));
+    for (int e = 0; e < 4; ++e) {
+      m[e] = mul2(m[e], pair(mi, mi));
+      const float2 d = in_reach(m[e], term[e]);
+      reach = max3_nan(reach, d.x, d.y);
+      const float2 vf = both(v[e]), r120 = both(mul2(v[e], pair(vi120, vi120)));
+      const uint32_t y0 = raised(r120.x, 2 * e), y1 = raised(r120.y, 2 * e + 1);
+      nearest_v = min(min(nearest_v, v_window(y0)), v_window(y1));
       // not to 0 from above it: a second moment of 0 beside a first moment that
       // is not would blow the next update up.  (The largest value's carry out of
       // the last code is next to a border.)
-      y[e] = max(y[e], min(__float_as_uint(v[e]), 1u) * least);
+      y[2 * e] = max(y0, min(__float_as_uint(vf.x), 1u) * least);
+      y[2 * e + 1] = max(y1, min(__float_as_uint(vf.y), 1u) * least);
     }
-    const bool near_m = __any_sync(kAll, nearest_m <= 0.f);
+    float mq[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = both(m[e]);
+      mq[2 * e] = f.x;
+      mq[2 * e + 1] = f.y;
+    }
+    const bool near_m = __any_sync(kAll, !(reach < 0.f)) && m_some;
     const bool near_v = far || __any_sync(kAll, nearest_v < (kVNear << 9));
     if (near_m || near_v) {
       const Exact z{a.beta1_64, a.beta2_64, k.clip64, ms, vs};
@@ -436,28 +503,33 @@ __global__ void __launch_bounds__(32 * kWarps, 4) adamw8_kernel(const __grid_con
         const float least_r = kE4m3Max * fmaf(w, -16.f * kUlp, 1.f);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (!(fabsf(m[e]) < least_r)) most = fmax(most, fabs(exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e])));
+          if (!(fabsf(mq[e]) < least_r)) most = fmax(most, fabs(exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e])));
         most = warp_max(most);
-        const double inv = m_some ? 448.0 / most : 0.0;
+        const double inv = 448.0 / most;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (clear_of_border(m[e], term[e]) <= 0.f) {
+        for (int e = 0; e < 8; ++e) {
+          const float2 d = in_reach(m[e / 2], term[e / 2]);
+          if (!((e & 1 ? d.y : d.x) < 0.f)) {
             const double r = exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e]) * inv;
             const double gap = e4m3_step(fabs(r));
-            m[e] = static_cast<float>(rint(r * inverse_of(gap)) * gap);
+            mq[e] = static_cast<float>(rint(r * inverse_of(gap)) * gap);
           }
+        }
       }
       if (near_v) {
         double most = 0;
-        const float least_r = far ? 0.f : kE4m3Max * (1.f - 32.f * kUlp);
+        const float least_v = far ? 0.f : vm * (1.f - 32.f * kUlp);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!(v[e] * vi < least_r)) most = fmax(most, exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]));
+        for (int e = 0; e < 8; ++e) {
+          const float2 vf = both(v[e / 2]);
+          if (!((e & 1 ? vf.y : vf.x) < least_v)) most = fmax(most, exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]));
+        }
         most = warp_max(most);
         const double inv = v_some ? 448.0 / most : 0.0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (far || v_window(raised(v[e], e)) < (kVNear << 9)) {
+        for (int e = 0; e < 8; ++e) {
+          const float2 r120 = both(mul2(v[e / 2], pair(vi120, vi120)));
+          if (far || v_window(raised(e & 1 ? r120.y : r120.x, e)) < (kVNear << 9)) {
             const double r = exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]) * inv;
             const double gap = e4m3_step(r);
             const double up =
@@ -465,10 +537,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4) adamw8_kernel(const __grid_con
             const uint32_t code = __float_as_uint(static_cast<float>(up) * 7.52316384526264e-37f) >> 20;
             y[e] = min(max(code, r > 0 ? 1u : 0u), 126u) << 24;
           }
+        }
       }
     }
     *cv = make_uint2(top_bytes(y[0], y[1], y[2], y[3]), top_bytes(y[4], y[5], y[6], y[7]));
-    *cm = pack_e4m3x8(m);
+    *cm = pack_e4m3x8(mq);
     if (lane == 0) {
       a.m_scale[q] = m_some ? mm * (1.f / kE4m3Max) : 0.f;
       a.v_scale[q] = v_some ? vm * (1.f / kE4m3Max) : 0.f;

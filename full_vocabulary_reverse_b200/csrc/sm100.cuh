@@ -341,4 +341,15 @@ __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
+// ---------------------------------------------------------------- launches that overlap
+// Lets the next launch of the stream (one with the attribute of a programmatic
+// dependent launch) begin as soon as every CTA of this grid has come here.
+__device__ __forceinline__ void let_next_launch_begin() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Waits until the launch before this one has finished and its writes are
+// visible (at once where this launch did not begin early).
+__device__ __forceinline__ void wait_for_last_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace rkl
