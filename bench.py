@@ -10,6 +10,12 @@ second.  With torchrun (N > 1) each rank runs an independent replica of the
 problem (no collective on the data path); the elapsed time is the max over
 ranks.
 
+`--train adamw` or `--train adamw8` times the whole training step of the
+workloads on the hidden payload instead: a gated feed-forward block (inner width
+3 H) in front of the head, the loss's forward and backward, the block's backward,
+and a clipped AdamW step (32-bit or 8-bit states, fp32 master weights) over the
+block's weights and the LM head.
+
 Rank 0 prints one JSON line.  `--impl reference` times the float64 CPU
 oracle (the reference arm) on a bounded sample of the same workload instead.
 """
@@ -33,6 +39,7 @@ import torch
 ROOT = os.path.dirname(os.path.abspath(__file__))
 sys.path.insert(0, ROOT)
 
+from full_vocabulary_reverse_b200 import AdamW, ffn_backward, ffn_forward  # noqa: E402
 from full_vocabulary_reverse_b200 import binding as rb  # noqa: E402
 from full_vocabulary_reverse_b200.workloads import WORKLOADS, make_workload  # noqa: E402
 
@@ -307,6 +314,41 @@ class Problem:
         return N
 
 
+class TrainProblem(Problem):
+    """A whole training step of a hidden-payload workload: the student's hidden
+    rows are the input of a gated block whose output the head projects; the
+    block's weights and the LM head train."""
+
+    def __init__(self, name, device, seed_offset=0, overrides=None, optimizer="adamw"):
+        super().__init__(name, device, seed_offset, overrides)
+        if path_of(self.cfg) != "hidden" or self.dt != rb.DT_BF16:
+            raise SystemExit("--train goes with the bf16 workloads on the hidden payload")
+        H, self.F = self.H, 3 * self.H
+        gen = torch.Generator(device=device).manual_seed(self.cfg["seed"] + seed_offset + 1)
+        w = lambda rows, cols: (torch.randn((rows, cols), generator=gen, device=device) * cols ** -0.5).bfloat16()  # noqa: E731
+        self.block = [w(self.F, H), w(self.F, H), w(H, self.F)]
+        self.optimizer = optimizer
+        self.opt = AdamW(self.block + [self.inp["W_s"]], lr=1e-5, weight_decay=0.1,
+                         state_bits=8 if optimizer == "adamw8" else 32, master_weights=True)
+
+    def step(self, h_s=None, teacher=None, mask=None, extra=None):
+        x = self.student if h_s is None else h_s
+        y, saved = ffn_forward(x, *self.block, save=True)
+        super().step(y, teacher, mask, extra)
+        _, *grads = ffn_backward(x, *self.block, self.dH.to(x.dtype), saved, needs=(False, True, True, True))
+        self.opt.step(grads + [self.dW], max_norm=1.0)
+
+    def work(self):
+        """Flops and bytes of one step's parts beside the loss's."""
+        T, H, F = self.T, self.H, self.F
+        n_block, n_head = 3 * F * H, self.V * H
+        grads = 2.0 * n_block + 4.0 * n_head  # bf16 and fp32
+        state = 4 if self.optimizer == "adamw8" else 16
+        return {"ffn_up_tc": ("tensor", 4.0 * T * F * H), "ffn_dgate_tc": ("tensor", 2.0 * T * F * H),
+                "ffn_gemm_tc": ("tensor", 8.0 * T * F * H), "norm_partial": ("hbm", grads),
+                self.optimizer: ("hbm", grads + (n_block + n_head) * (2.0 + 8.0 + state))}
+
+
 def reduce_over_ranks(ms, tokens, dist, device):
     """(max over ranks of the device-timed milliseconds, sum over ranks of the tokens)."""
     t = torch.tensor([float(ms)], dtype=torch.float64, device=device)
@@ -503,7 +545,10 @@ def run_reference(args, rank, world):
 def run_gpu(args, rank, world, dist):
     dev = torch.device("cuda", int(os.environ.get("LOCAL_RANK", 0)))
     torch.cuda.set_device(dev)
-    prob = Problem(args.workload, dev, seed_offset=rank, overrides=shape_overrides(args))
+    if args.train:
+        prob = TrainProblem(args.workload, dev, rank, shape_overrides(args), args.train)
+    else:
+        prob = Problem(args.workload, dev, seed_offset=rank, overrides=shape_overrides(args))
     L = rb.lib()
     stream = torch.cuda.current_stream()
 
@@ -606,7 +651,7 @@ def run_gpu(args, rank, world, dist):
     if rank != 0:
         return
     pk = peaks()
-    work = algorithmic_work(prob, N)
+    work = dict(algorithmic_work(prob, N), **(prob.work() if args.train else {}))
     # dominant kernel = the one with the largest share of device time
     dom = max((k for k in prof if k in work), key=lambda k: prof[k]["ms"])
     bound, per_step = work[dom]
@@ -690,7 +735,9 @@ def run_gpu(args, rank, world, dist):
                     ", N and per-teacher counts" if prob.multi else "")},
         "gpu_launches": int(launches),
     }
-    if world == 1 and not args.no_cpu_baseline:
+    if args.train:
+        out["config"]["train"] = "gated block (F = %d) + loss + clipped %s step" % (prob.F, args.train)
+    if world == 1 and not args.no_cpu_baseline and not args.train:
         inp = dict(prob.inp)
         out["cpu_baseline"] = {k: v for k, v in cpu_oracle_sample(inp, prob.reduction, prob.name, k=prob.k).items()
                                if k not in ("seconds", "rows")}
@@ -712,6 +759,7 @@ def main():
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--workload", default="qwen_hidden", choices=sorted(WORKLOADS))
+    ap.add_argument("--train", choices=("adamw", "adamw8"), help="time the whole training step with this optimizer")
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--ref-rows", type=int, default=32)
     ap.add_argument("--no-cpu-baseline", action="store_true")
