@@ -1463,9 +1463,11 @@ static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bo
                                bool b_mn, void* C, int64_t M, int64_t N, int64_t K, bool up, int parts, int part_rows) {
   FfnPairProduct& p = a.p[a.n++];
   RKL_TRY(operand_map(&p.a[0], A, a_mn ? K : M, a_mn ? M : K, a_mn));
-  RKL_TRY(operand_map(&p.a[1], A2 ? A2 : A, a_mn ? K : M, a_mn ? M : K, a_mn));
+  p.a[1] = p.a[0];
+  if (A2) RKL_TRY(operand_map(&p.a[1], A2, a_mn ? K : M, a_mn ? M : K, a_mn));
   RKL_TRY(operand_map(&p.b[0], B, b_mn ? K : N, b_mn ? N : K, b_mn));
-  RKL_TRY(operand_map(&p.b[1], B2 ? B2 : B, b_mn ? K : N, b_mn ? N : K, b_mn));
+  p.b[1] = p.b[0];
+  if (B2) RKL_TRY(operand_map(&p.b[1], B2, b_mn ? K : N, b_mn ? N : K, b_mn));
   if (parts > 1)
     RKL_TRY(make_map(&p.c, C, true, N, int64_t(parts) * part_rows, N * 4, 32, 32));
   else
@@ -1490,7 +1492,8 @@ static rkl_status skinny_product(const SkinnyPlan& p, const void* x, const void*
   FfnSkinnyArgs a = {};
   a.cols = static_cast<int>((T + 15) / 16 * 16);
   RKL_TRY(operand_map(&a.w1, W1, R1, K, false));
-  RKL_TRY(operand_map(&a.w2, W2 ? W2 : W1, R1, K, false));
+  a.w2 = a.w1;
+  if (W2) RKL_TRY(operand_map(&a.w2, W2, R1, K, false));
   RKL_TRY(make_map(&a.x, x, false, K, T, K * 2, kBK, a.cols));
   a.part = part;
   a.per = p.per;

@@ -502,6 +502,15 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
   const long long all = static_cast<long long>(a.tiles) * a.steps;
   const long long hi = lo + a.per < all ? lo + a.per : all;
 
+  const int first_tile = static_cast<int>(lo / a.steps), first_k = static_cast<int>(lo % a.steps);
+  const int early = hi - lo < a.stages ? static_cast<int>(hi - lo) : a.stages;
+  auto load_w = [&](int st, int tile, int k) {
+    const bool second = tile >= a.tiles_first;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    tma_load_2d(smem + st * stage_bytes, second ? &a.w2 : &a.w1, &full[st], k * kBK,
+                (second ? tile - a.tiles_first : tile) * 128);
+  };
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&full[i], 1);
@@ -514,6 +523,16 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
     mbar_init(tear, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    // The weights do not depend on the launch before this one, x and the parts'
+    // memory may: the ring fills with weights at once, up to 216 KB on each SM
+    // while that launch ends and this one gets ready.
+    for (int i = 0, t = first_tile, k = first_k; i < early; ++i) {
+      load_w(i, t, k);
+      if (++k == a.steps) {
+        k = 0;
+        ++t;
+      }
+    }
   }
   if (warp == 2) {
     tmem_alloc(tmem_holder, kSkinnyTmem);
@@ -527,29 +546,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
 
   if (warp == 0) {
     if (lane == 0) {
-      // The weights do not depend on the launch before this one, x and the
-      // parts' memory may: the ring fills with weights first, up to 216 KB on
-      // each SM while that launch ends.
-      auto load_w = [&](int st, int tile, int k) {
-        const bool second = tile >= a.tiles_first;
-        mbar_arrive_expect_tx(&full[st], stage_bytes);
-        tma_load_2d(smem + st * stage_bytes, second ? &a.w2 : &a.w1, &full[st], k * kBK,
-                    (second ? tile - a.tiles_first : tile) * 128);
-      };
       auto load_x = [&](int st, int k) {
         tma_load_2d(smem + st * stage_bytes + kOperand, &a.x, &full[st], k * kBK, 0);
       };
       int stage = 0;
       uint32_t phase = 0, armed = 0, last_par = 0;
-      int tile = static_cast<int>(lo / a.steps), k = static_cast<int>(lo % a.steps);
-      const int early = hi - lo < a.stages ? static_cast<int>(hi - lo) : a.stages;
-      for (int i = 0, t = tile, kk = k; i < early; ++i) {
-        load_w(i, t, kk);
-        if (++kk == a.steps) {
-          kk = 0;
-          ++t;
-        }
-      }
+      int tile = first_tile, k = first_k;
       wait_for_last_launch();
       for (long long s = lo; s < hi; ++s) {
         if (!RKL_BOUNDS(tile < a.tiles && k < a.steps)) {
@@ -583,43 +585,49 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      // What a step costs here besides its bytes is this loop's own latency: it
+      // holds nothing that can be settled outside.  A stage's descriptors are
+      // the first one's with the address moved, 16 deep slices 32 B on.
       const uint32_t idesc = idesc_bf16(128, a.cols, 0, 0);
+      const uint64_t first_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const int stages = a.stages, steps = a.steps, stage_desc = stage_bytes >> 4;
       int stage = 0;
+      uint64_t desc = first_desc;
       uint32_t phase = 0;
-      int k = static_cast<int>(lo % a.steps);
-      uint32_t more = 0;
+      bool ok = true;
+      int k = first_k;
       int i = 0;  // accumulators handed over
-      for (long long s = lo; s < hi; ++s) {
-        const int acc = i & 1;
-        if (!more) {
-          if (!mbar_wait(&acc_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag)) {
-            give_up(abort_flag, ERR_WAIT_ACC_EMPTY);
-            break;
-          }
-          tc_fence_after();
-        }
-        if (!mbar_wait(&full[stage], phase, abort_flag)) {
-          give_up(abort_flag, ERR_WAIT_TMA_FULL);
+      for (int left = static_cast<int>(hi - lo); left > 0 && ok; ++i) {
+        const int acc = i & 1, n = left < steps - k ? left : steps - k;
+        const uint32_t d = tmem_base + acc * kFfnSkinnyRows;
+        if (!mbar_wait(&acc_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag)) {
+          give_up(abort_flag, ERR_WAIT_ACC_EMPTY);
           break;
         }
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + stage * stage_bytes), sb = sa + kOperand;
+        uint32_t more = 0;
+        for (int x = 0; x < n; ++x) {
+          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+            give_up(abort_flag, ERR_WAIT_TMA_FULL);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < kBK / 16; ++j)
-          umma_bf16(tmem_base + acc * kFfnSkinnyRows, sdesc_sw128(sa + 32 * j, 16, 1024),
-                    sdesc_sw128(sb + 32 * j, 16, 1024), idesc, more | j);
-        more = 1;
-        umma_commit(&empty[stage]);
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1;
+          for (int j = 0; j < kBK / 16; ++j)
+            umma_bf16(d, desc + 2 * j, desc + (kOperand >> 4) + 2 * j, idesc, more | j);
+          more = 1;
+          umma_commit(&empty[stage]);
+          desc += stage_desc;
+          if (++stage == stages) {
+            stage = 0;
+            desc = first_desc;
+            phase ^= 1;
+          }
         }
-        if (++k == a.steps || s + 1 == hi) {
-          umma_commit(&acc_full[acc]);
-          k = 0;
-          more = 0;
-          ++i;
-        }
+        if (ok) umma_commit(&acc_full[acc]);
+        left -= n;
+        k = 0;
       }
       umma_commit(tear);
       volatile int never = 0;

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 from array import array
 from functools import lru_cache
+from operator import attrgetter
 
 import torch
 
@@ -41,6 +42,18 @@ def _norm_workspace_size(n):
     nbytes = ctypes.c_size_t(0)
     _check(lib().rkl_grad_norm_workspace_size(n, ctypes.byref(nbytes)))
     return nbytes.value
+
+
+_shape = attrgetter("shape")
+_layout = attrgetter("layout")
+_strided = {torch.strided}
+
+
+def _alike(tensors, shapes, index):
+    """Whether all are dense and contiguous, of these shapes (None: any), on
+    device `index`."""
+    return (set(map(_layout, tensors)) == _strided and set(map(torch.Tensor.get_device, tensors)) == {index} and
+            all(map(torch.Tensor.is_contiguous, tensors)) and (shapes is None or list(map(_shape, tensors)) == shapes))
 
 
 def _norm_into(n, ptrs, numel, codes, device):
@@ -73,12 +86,15 @@ def grad_norm(grads):
         raise RKLError(2, "grad_norm needs a gradient")
     device = grads[0].device
     index = grads[0].get_device()
-    for g in grads:
-        if not g.is_cuda or g.get_device() != index or g.is_sparse:
-            raise RKLError(2, "gradients must be dense CUDA tensors on one device")
-    codes = _dtype_codes(grads, "gradient")
+    if not all(g.is_cuda for g in grads):
+        raise RKLError(2, "gradients must be CUDA tensors")
     with _on_device(index):
-        grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
+        if not _alike(grads, None, index):
+            for g in grads:
+                if g.get_device() != index or g.layout != torch.strided:
+                    raise RKLError(2, "gradients must be dense tensors on one device")
+            grads = [g.contiguous() for g in grads]
+        codes = _dtype_codes(grads, "gradient")
         return _norm_into(len(grads), array("Q", [g.data_ptr() for g in grads]), array("q", [g.numel() for g in grads]), codes,
                           device)
 
@@ -183,16 +199,10 @@ class AdamW:
         if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != device):
             raise RKLError(2, "norm must be a 1-element float32 tensor beside the parameters")
         index = device.index
-        ptrs = array("Q", bytes(8 * n))
         with _on_device(index):
-            for i, (g, shape) in enumerate(zip(grads, self._shapes)):
-                if g is None:
-                    continue
-                if g.shape != shape or g.get_device() != index or g.is_sparse:
-                    raise RKLError(2, "gradient %d must be a dense tensor of its parameter's shape and device" % i)
-                if not g.is_contiguous():
-                    g = grads[i] = g.contiguous()
-                ptrs[i] = g.data_ptr()
+            if any(g is None for g in grads) or not _alike(grads, self._shapes, index):
+                grads = self._each_checked(grads, index)
+            ptrs = array("Q", [0 if g is None else g.data_ptr() for g in grads])
             codes = _dtype_codes(grads, "gradient")
             if max_norm is not None and norm is None:
                 norm = _norm_into(n, ptrs, self._numel, codes, device)
@@ -209,6 +219,17 @@ class AdamW:
         if self._tracked:
             torch.autograd.graph.increment_version(self._tracked)
         return norm
+
+    def _each_checked(self, grads, index):
+        """The gradients one by one: contiguous, or the reason why not."""
+        out = []
+        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+            if g is not None:
+                if g.shape != shape or g.get_device() != index or g.layout != torch.strided:
+                    raise RKLError(2, "gradient %d must be a dense tensor of its parameter's shape and device" % i)
+                g = g.contiguous()
+            out.append(g)
+        return out
 
     def moments(self, i):
         """(exp_avg, exp_avg_sq) of parameter i as fp32 tensors of its shape."""
