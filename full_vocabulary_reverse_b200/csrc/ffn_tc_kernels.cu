@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(ring + kRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
 
@@ -275,18 +275,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           }
     }
   } else if (warp == 1) {
-    if (leader && lane == 0) {
+    if (leader) {  // the whole warp runs the loop, one lane issues
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int slot = i % kRing;
-        if (!mbar_wait(&ring_full[slot], (i / kRing) & 1, abort_flag)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ring_full[slot], (i / kRing) & 1, abort_flag))) {
           give_up(abort_flag, ERR_WAIT_AUX);
           break;
         }
-        const int t = ring[slot];
-        mbar_arrive(&ring_empty[slot]);
+        const int t = __shfl_sync(0xffffffffu, ring[slot], 0);
+        if (lane == 0) mbar_arrive(&ring_empty[slot]);
+        __syncwarp();
         if (t < 0) break;
         const Item it = item_of(a, t);
         const FfnPairProduct& p = a.p[it.q];
@@ -295,44 +296,48 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
         // swizzled row; MN-major: 16 rows of 128 B, the 64-wide blocks
         // kOperand / 2 apart.
         const uint32_t idesc = idesc_bf16(256, 256, p.a_mn, p.b_mn);
-        const uint32_t a_step = p.a_mn ? 2048u : 32u, a_lbo = p.a_mn ? kOperand / 2 : 16u;
-        const uint32_t b_step = p.b_mn ? 2048u : 32u, b_lbo = p.b_mn ? kOperand / 2 : 16u;
+        const uint32_t a_step = p.a_mn ? 2048u >> 4 : 32u >> 4, b_step = p.b_mn ? 2048u >> 4 : 32u >> 4;
+        const uint64_t a_desc = sdesc_sw128(smem_u32(smem), p.a_mn ? kOperand / 2 : 16u, 1024);
+        const uint64_t b_desc = sdesc_sw128(smem_u32(smem) + kOperand, p.b_mn ? kOperand / 2 : 16u, 1024);
         const int acc = i & 1;
         const uint32_t d = tmem_base + acc * 256;
-        if (!mbar_wait_cluster(&acc_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag))) {
           give_up(abort_flag, ERR_WAIT_ACC_EMPTY);
           break;
         }
         tc_fence_after();
         uint32_t more = 0;
         for (int s = it.lo; s < it.hi; ++s) {
-          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag));
+          if (!ok) {
             give_up(abort_flag, ERR_WAIT_TMA_FULL);
-            ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t base = smem_u32(smem + stage * kPairStage);
+          const uint32_t at = stage * (kPairStage >> 4);  // of the stage, in the descriptors' 16-byte units
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) {
-              const uint32_t sa = base + h * kHalfStage, sb = sa + kOperand;
-              umma_bf16_pair(d, sdesc_sw128(sa + a_step * k, a_lbo, 1024), sdesc_sw128(sb + b_step * k, b_lbo, 1024),
-                             idesc, more | h | k);
-            }
+              for (int k = 0; k < kBK / 16; ++k)
+                umma_bf16_pair(d, a_desc + (at + h * (kHalfStage >> 4) + a_step * k),
+                               b_desc + (at + h * (kHalfStage >> 4) + b_step * k), idesc, more | h | k);
+            umma_commit_pair(&empty[stage], 0x3);
+          }
           more = 1;
-          umma_commit_pair(&empty[stage], 0x3);
           if (++stage == kPairStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (ok) umma_commit_pair(&acc_full[acc], 0x3);
+        if (ok && elect_one()) umma_commit_pair(&acc_full[acc], 0x3);
       }
-      umma_commit_pair(tear, 0x1);
-      volatile int never = 0;
-      if (!mbar_wait(tear, 0, &never)) atomicOr(&g_ffn_err, ERR_WAIT_TEARDOWN);
+      if (elect_one()) {
+        umma_commit_pair(tear, 0x1);
+        volatile int never = 0;
+        if (!mbar_wait(tear, 0, &never)) atomicOr(&g_ffn_err, ERR_WAIT_TEARDOWN);
+      }
+      __syncwarp();
     }
   } else {
     const int quarter = warp & 3;
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tear + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const long long lo = static_cast<long long>(blockIdx.x) * a.per;
   const long long all = static_cast<long long>(a.tiles) * a.steps;
   const long long hi = lo + a.per < all ? lo + a.per : all;
@@ -584,55 +589,60 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1) ffn_skinny_kernel(const __g
         }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // What a step costs here besides its bytes is this loop's own latency: it
-      // holds nothing that can be settled outside.  A stage's descriptors are
-      // the first one's with the address moved, 16 deep slices 32 B on.
-      const uint32_t idesc = idesc_bf16(128, a.cols, 0, 0);
-      const uint64_t first_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
-      const int stages = a.stages, steps = a.steps, stage_desc = stage_bytes >> 4;
-      int stage = 0;
-      uint64_t desc = first_desc;
-      uint32_t phase = 0;
-      bool ok = true;
-      int k = first_k;
-      int i = 0;  // accumulators handed over
-      for (int left = static_cast<int>(hi - lo); left > 0 && ok; ++i) {
-        const int acc = i & 1, n = left < steps - k ? left : steps - k;
-        const uint32_t d = tmem_base + acc * kFfnSkinnyRows;
-        if (!mbar_wait(&acc_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag)) {
-          give_up(abort_flag, ERR_WAIT_ACC_EMPTY);
+    // The whole warp runs the loop and one lane issues: the MMAs' operands then
+    // live in uniform registers.  What a step costs here besides its bytes is
+    // this loop's own latency, so it holds nothing that can be settled outside.
+    // A stage's descriptors are the first one's with the address moved, slices
+    // of 16 lie 32 B apart.
+    const uint32_t idesc = idesc_bf16(128, a.cols, 0, 0);
+    const uint64_t first_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const int stages = a.stages, steps = a.steps, stage_desc = stage_bytes >> 4;
+    int stage = 0;
+    uint64_t desc = first_desc;
+    uint32_t phase = 0;
+    bool ok = true;
+    int k = first_k;
+    int i = 0;  // accumulators handed over
+    for (int left = static_cast<int>(hi - lo); left > 0 && ok; ++i) {
+      const int acc = i & 1, n = left < steps - k ? left : steps - k;
+      const uint32_t d = tmem_base + acc * kFfnSkinnyRows;
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[acc], ((i >> 1) & 1) ^ 1, abort_flag))) {
+        give_up(abort_flag, ERR_WAIT_ACC_EMPTY);
+        break;
+      }
+      tc_fence_after();
+      uint32_t more = 0;
+      for (int x = 0; x < n; ++x) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, abort_flag));
+        if (!ok) {
+          give_up(abort_flag, ERR_WAIT_TMA_FULL);
           break;
         }
         tc_fence_after();
-        uint32_t more = 0;
-        for (int x = 0; x < n; ++x) {
-          if (!mbar_wait(&full[stage], phase, abort_flag)) {
-            give_up(abort_flag, ERR_WAIT_TMA_FULL);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j)
             umma_bf16(d, desc + 2 * j, desc + (kOperand >> 4) + 2 * j, idesc, more | j);
-          more = 1;
           umma_commit(&empty[stage]);
-          desc += stage_desc;
-          if (++stage == stages) {
-            stage = 0;
-            desc = first_desc;
-            phase ^= 1;
-          }
         }
-        if (ok) umma_commit(&acc_full[acc]);
-        left -= n;
-        k = 0;
+        more = 1;
+        desc += stage_desc;
+        if (++stage == stages) {
+          stage = 0;
+          desc = first_desc;
+          phase ^= 1;
+        }
       }
+      if (ok && elect_one()) umma_commit(&acc_full[acc]);
+      left -= n;
+      k = 0;
+    }
+    if (elect_one()) {
       umma_commit(tear);
       volatile int never = 0;
       if (!mbar_wait(tear, 0, &never)) atomicOr(&g_ffn_err, ERR_WAIT_TEARDOWN);
     }
+    __syncwarp();
   } else {
     wait_for_last_launch();
     const int quarter = warp & 3;
