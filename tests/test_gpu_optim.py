@@ -279,6 +279,50 @@ def test_stochastic_rounding_follows_a_slow_moment():
     assert abs(mean - want) <= bound, (mean, want, bound)
 
 
+def test_codes_are_the_formulas_everywhere():
+    """Every one of a million codes, over steps of steady, growing, vanishing and cancelling gradients, is the one that
+    64-bit arithmetic gives: fp32's error never picks the neighbour."""
+
+    def same(codes, ref):
+        # Values of bf16 gradients can lie on a border exactly (the first step's m is 0.1 g: a ratio of two bf16
+        # numbers); there the order of the reference's own operations decides.  A value is off by a few 2^-53 of
+        # itself, at most 16 code steps: below 2^-40 of a step.
+        value, _, edge, _, _ = ref
+        return not ((codes.double().cpu() != value) & (edge > 2.0 ** -40)).any()
+    n = 1 << 20
+    gen = torch.Generator().manual_seed(6)
+    base = torch.randn(n, generator=gen) * torch.exp(2 * torch.randn(n, generator=gen))
+    p = torch.zeros(n, device="cuda")
+    opt = AdamW([p], lr=1e-3, betas=BETAS, weight_decay=0.0, state_bits=8, seed=77)
+    where = torch.arange(n)
+    for t, factor in enumerate([1.0, 1.0, 1.0, -7.0, 1e-3, 30.0, 1.0, 1e4, -3e-2, 1.0], 1):
+        g = (base * factor * 1e-3).bfloat16().cuda()
+        _, m0, v0 = state64(opt, 0)
+        norm = opt.step([g], max_norm=1.0)
+        g64 = g.double().cpu() * min(1.0, 1.0 / float(norm))
+        _, m, v = R.adamw(torch.zeros_like(m0), m0, v0, g64, t, 1e-3, BETAS, EPS, 0.0)
+        assert same(opt.exp_avg, R.codes(m)), t
+        assert same(opt.exp_avg_sq, R.codes(v, R.random20(where, t, 77))), t
+
+
+def test_large_and_tiny_moments_in_8_bits():
+    """Gradients up to the end of fp32's range and below its squares' range: codes by the formula, blocks too small for
+    a scale held as zeros."""
+    sizes = [1e-18, 1e-10, 1.0, 1e4, 1e9, 1e18]
+    n = 256 * len(sizes)
+    gen = torch.Generator().manual_seed(2)
+    g = (torch.randn(len(sizes), 256, generator=gen) * torch.tensor(sizes)[:, None]).view(-1).cuda()
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=1e-3, betas=BETAS, weight_decay=0.0, state_bits=8, seed=3)
+    for t in (1, 2):
+        _, m0, v0 = state64(opt, 0)
+        opt.step([g])
+        _, m, v = R.adamw(torch.zeros_like(m0), m0, v0, g.double().cpu(), t, 1e-3, BETAS, EPS, 0.0)
+        assert torch.equal(opt.exp_avg.double().cpu(), R.codes(m)[0])
+        assert torch.equal(opt.exp_avg_sq.double().cpu(), R.codes(v, R.random20(torch.arange(n), t, 3))[0])
+    assert not opt.exp_avg_sq[:256].view(torch.uint8).any() and opt.exp_avg[:256].view(torch.uint8).any()
+    assert opt.params[0].isfinite().all()
+
+
 def test_places_past_32_bits():
     n = (1 << 31) + 300
     if torch.cuda.mem_get_info()[0] < 24 << 30:
