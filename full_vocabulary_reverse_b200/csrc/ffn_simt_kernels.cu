@@ -19,7 +19,9 @@
 // multiply-adds (4 x 4 results a thread, 8 for 4, ran half as fast).  BT = 128
 // where there are many tiles; else 64, whose 64 threads of results are four
 // times over, each for a quarter of every slice, and add up at the end: with
-// one tile an SM, 2 warps alone took twice as long.
+// one tile an SM, 2 warps alone took twice as long.  fp32 forward and backward:
+// T = 509, H = O = 515, F = 1031 in 0.25 ms (19 TFLOP/s), T = 4096, H = O = 2048,
+// F = 4096 in 13.5 (46; a library's fp32 products run at 56).
 #include <cuda_bf16.h>
 
 #include "ffn_act.cuh"

@@ -26,8 +26,17 @@
 // borders lie in it, and leaves fp32 parts that a small kernel joins in a fixed
 // order (with the activation between the two halves of the block).
 //
-// Bounds: ffn_pair_kernel by the tensor pipe (512 SM cycles for a 256 x 256 x
-// 64 step), ffn_skinny_kernel by HBM.
+// What bounds them, with T = 8192, H = O = 2048, F = 6144:
+//   UP    0.30 ms (1.39 PFLOP/s; the tensor pipe needs 512 SM cycles for a 256 x
+//         256 x 64 step), 0.37 with g and u stored beside it (403 MB)
+//   DGATE 0.23 ms: 206 GFLOP, but 760 MB through memory, g and u most of it.  In
+//         row-major order each lane's 16 bytes lay in a line of their own and the
+//         same work took 0.48 ms; hence the blocks of ffn_saved_at
+//   GEMM  0.15 ms for y, 0.75 for the four backward products (1.38 PFLOP/s)
+// together as much as the power limit leaves (a library product runs at 1.40
+// sustained).  ffn_skinny_kernel by HBM where the weights are large: 181 MB
+// (H = 4096, F = 11008, 23 rows) in 30 us, and by its start-up, some 5 us, where
+// they are small.
 #include <cuda_bf16.h>
 
 #include "bounds.cuh"

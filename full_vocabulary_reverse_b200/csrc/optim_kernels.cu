@@ -15,9 +15,9 @@
 // The 8-bit form holds a block as 256 e4m3 codes and one fp32 scale (largest
 // magnitude / 448), so the warp that updates a block also finds its scale.
 //
-// Both kernels are bound by memory: they touch every byte once.  The tables of
-// tensors travel in the kernel's parameters (up to kOptTensors a launch), so a
-// step needs no copy to the device and can be captured in a graph.
+// Every byte is touched once.  The tables of tensors travel in the kernels'
+// parameters (up to kOptTensors a launch), so a step needs no copy to the device
+// and can be captured in a graph.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -303,7 +303,8 @@ __device__ __forceinline__ float new_param(float p, float m, float v, float keep
 }  // namespace
 
 // 32-bit moments.  Bound by memory: 30 bytes an element with bf16 parameters,
-// master copies and fp32 gradients.
+// master copies and fp32 gradients, moved at 6.2 TB/s (349 M elements in 1.68
+// ms; a plain copy runs at 6.55).
 __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constant__ AdamwArgs a) {
   __shared__ StepConsts k;
   begin_step(a, &k);
@@ -345,9 +346,13 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
   }
 }
 
-// 8-bit moments: 8 bytes an element with bf16 parameters and gradients.  The
-// arithmetic (about 70 instructions an element, most of them the codes') and
-// not memory sets the time.
+// 8-bit moments: 10 bytes an element with bf16 parameters and gradients.  The
+// arithmetic (about 70 instructions an element, most of them the codes' and the
+// random numbers') and not memory sets the time: 349 M elements take 1.0 to 1.35
+// ms, by how many blocks look again in 64 bits (2 in 100 on changing gradients,
+// about 15 where the gradient stays the same and moments stop next to borders).
+// Paired fp32 instructions took 10 % of the instructions away; 24 warps an SM
+// with the next block's lines on their way to L2 ran faster than 16 or 32.
 //
 // Beside the codes, fp32 arithmetic finds the values that lie within its error
 // of a border between two codes; their block then looks at those again in 64
@@ -584,7 +589,8 @@ __device__ __forceinline__ double block_sum(double d) {
 
 // Each block sums the squares of every gridDim.x-th chunk of kNormChunk
 // elements, in a fixed order, into one partial sum: no atomics, so the same
-// gradients give the same norm bit for bit.
+// gradients give the same norm bit for bit.  Bound by memory: 349 M bf16
+// elements in 105 us, 6.6 TB/s.
 __global__ void __launch_bounds__(32 * kWarps) norm_partial_kernel(const __grid_constant__ NormArgs a) {
   const int lane = threadIdx.x & 31;
   double sum = 0.0;
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_partial_kernel(const __grid_
     const long long i = static_cast<long long>(b - a.first[t]) * kNormChunk + lane * 8;
     if (!RKL_BOUNDS(i >= 0 && i < x.n + kNormChunk)) continue;
     // A chunk inside the tensor: all its loads are in flight before the first
-    // sum (behind a test each, they went one by one: 3.7 TB/s).
+    // sum (behind a test each they went one by one, at 3.7 TB/s).
     if ((x.flags & OPT_WIDE_GRAD) && i - lane * 8 + kNormChunk <= x.n) {
       if (x.flags & OPT_GRAD_BF16) {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x.grad) + i);
