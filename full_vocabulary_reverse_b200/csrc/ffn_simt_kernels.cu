@@ -7,8 +7,8 @@
 //   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T a
 //
 // One tiled product kernel does all of them: C(m, n) = sum_k A(m, k) B(k, n)
-// with any strides, BT x BT tiles, 16 deep, the next slices' loads under way
-// while the present one is multiplied.  A thread owns 8 x 8 results: rows and
+// with any strides, BT x BT tiles, the next slice's loads under way while
+// the present one is multiplied.  A thread owns 8 x 8 results: rows and
 // columns in two groups of 4, BT / 2 apart.  So the up form puts Wg's columns in
 // the tile's first half and Wu's in the second, and a thread holds g and u of
 // the same elements: the activation, the product and the rounding happen in its
@@ -30,13 +30,14 @@
 namespace rkl {
 namespace {
 
-constexpr int kDepth = 16;
 constexpr int kResults = 8;  // of a thread, each way
 constexpr int kSimtThreads = 256;
 template <int BT>
+constexpr int kDepth = BT == 64 ? 32 : 16;  // of a slice of K (the small tile has fewer instructions between barriers)
+template <int BT>
 constexpr int kGroups = kSimtThreads / ((BT / kResults) * (BT / kResults));  // of threads that share a tile's K
 template <int BT>
-constexpr int kShare = BT * kDepth / kSimtThreads;  // elements of an operand's slice that a thread moves
+constexpr int kShare = BT * kDepth<BT> / kSimtThreads;  // elements of an operand's slice that a thread moves
 
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
@@ -67,8 +68,8 @@ __device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
 template <int BT>
 __device__ __forceinline__ void slice_place(bool k_fast, int i, int* mn, int* k) {
   const int e = threadIdx.x + i * kSimtThreads;
-  *k = k_fast ? e % kDepth : e / BT;
-  *mn = k_fast ? e / kDepth : e % BT;
+  *k = k_fast ? e % kDepth<BT> : e / BT;
+  *mn = k_fast ? e / kDepth<BT> : e % BT;
 }
 
 // This thread's share of an operand's slices: position `mn` of the tile is row
@@ -105,8 +106,8 @@ struct Operand {
     return ((upper >> i) & 1 ? p2 : p) + offset[i];
   }
   __device__ __forceinline__ void advance() {
-    p += kDepth * s_k;
-    p2 += kDepth * s_k;
+    p += kDepth<BT> * s_k;
+    p2 += kDepth<BT> * s_k;
   }
 };
 
@@ -179,11 +180,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
   constexpr int STEP = BT / 2;  // between a thread's groups of 4
   constexpr int BN = MODE == FFN_UP ? BT / 2 : BT;  // result columns of a tile
   constexpr bool kAsync = sizeof(T) == 4;
-  // Slices in flight.  The small tile multiplies a slice in less time than a read
-  // from memory takes: three are under way behind the present one.
-  constexpr int RING = BT == 64 ? 4 : 2;
-  __shared__ __align__(16) float sa[RING][kDepth][BT + 4];
-  __shared__ __align__(16) float sb[RING][kDepth][BT + 4];
+  constexpr int RING = 2;  // one slice is multiplied, the next is on its way
+  __shared__ __align__(16) float sa[RING][kDepth<BT>][BT + 4];
+  __shared__ __align__(16) float sb[RING][kDepth<BT>][BT + 4];
   static_assert(kGroups<BT> == 1 || sizeof(sa) >= size_t(BT) * BT * 4, "a group's sums fit into sa or sb");
 
   int q = 0;
@@ -204,13 +203,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
   Operand<T, BT> oa(p.a[0], nullptr, p.sam, p.sak, m0, p.M, 0);
   Operand<T, BT> ob(p.b[0], p.b[1], p.sbn, p.sbk, n0, p.N, MODE == FFN_UP ? BN : 0);
   // Slices of all segments of K, one behind another; the loads run ahead.
-  const int per_segment = static_cast<int>((p.K + kDepth - 1) / kDepth);
+  const int per_segment = static_cast<int>((p.K + kDepth<BT> - 1) / kDepth<BT>);
   const int slices = per_segment * p.segments;
   int ahead = 0;                     // next slice to load
   int left = static_cast<int>(p.K);  // positions along k from it to its segment's end
   auto advance = [&] {
     ++ahead;
-    left -= kDepth;
+    left -= kDepth<BT>;
     oa.advance();
     ob.advance();
     if (ahead == per_segment && p.segments == 2) {
@@ -221,8 +220,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
   };
   auto multiply = [&](int slot) {
 #pragma unroll
-    for (int d = 0; d < kDepth / kGroups<BT>; ++d) {
-      const int k = group * (kDepth / kGroups<BT>) + d;
+    for (int d = 0; d < kDepth<BT> / kGroups<BT>; ++d) {
+      const int k = group * (kDepth<BT> / kGroups<BT>) + d;
       float x[R];
       uint64_t w[R / 2];
 #pragma unroll
