@@ -1373,10 +1373,8 @@ static SkinnyPlan skinny_plan(int64_t rows_first, int64_t rows_second, int64_t K
   p.per = (all + kPlanSms - 1) / kPlanSms;
   if (p.per < 4) p.per = 4;
   p.grid = static_cast<int>((all + p.per - 1) / p.per);
-  for (long long t = 0; t < p.tiles; ++t) {
-    const int n = static_cast<int>(((t + 1) * p.steps - 1) / p.per - t * p.steps / p.per) + 1;
-    if (n > p.parts) p.parts = n;
-  }
+  // a tile of `steps` that begins anywhere in a CTA's share touches this many CTAs at most
+  p.parts = static_cast<int>((p.steps - 2 + p.per) / p.per) + 1;
   p.pitch = p.tiles * 128;
   return p;
 }
