@@ -45,15 +45,17 @@ def _norm_workspace_size(n):
 
 
 _shape = attrgetter("shape")
-_layout = attrgetter("layout")
-_strided = {torch.strided}
 
 
-def _alike(tensors, shapes, index):
-    """Whether all are dense and contiguous, of these shapes (None: any), on
-    device `index`."""
-    return (set(map(_layout, tensors)) == _strided and set(map(torch.Tensor.get_device, tensors)) == {index} and
-            all(map(torch.Tensor.is_contiguous, tensors)) and (shapes is None or list(map(_shape, tensors)) == shapes))
+def _plain(tensors, shapes, index):
+    """Whether all are dense and contiguous tensors of these shapes (None: any)
+    on device `index`; False where one has to be looked at by itself."""
+    try:
+        return (all(map(torch.Tensor.is_contiguous, tensors)) and
+                set(map(torch.Tensor.get_device, tensors)) == {index} and
+                (shapes is None or list(map(_shape, tensors)) == shapes))
+    except (RuntimeError, TypeError):  # no layout with strides; a None
+        return False
 
 
 def _norm_into(n, ptrs, numel, codes, device):
@@ -68,13 +70,19 @@ def _norm_into(n, ptrs, numel, codes, device):
     return norm
 
 
+@lru_cache(maxsize=64)
+def _codes_of(dtypes):
+    return array("i", [_CODES[d] for d in dtypes])
+
+
 def _dtype_codes(tensors, what):
     """Their dtype codes as an array (of a ``None``: fp32's)."""
     try:
-        return array("i", [DT_FP32 if t is None else _CODES[t.dtype] for t in tensors])
+        return _codes_of(tuple([torch.float32 if t is None else t.dtype for t in tensors]))
     except KeyError:
         for i, t in enumerate(tensors):
-            _code(t, "%s %d" % (what, i))
+            if t is not None:
+                _code(t, "%s %d" % (what, i))
         raise
 
 
@@ -86,10 +94,10 @@ def grad_norm(grads):
         raise RKLError(2, "grad_norm needs a gradient")
     device = grads[0].device
     index = grads[0].get_device()
-    if not all(g.is_cuda for g in grads):
+    if index < 0:
         raise RKLError(2, "gradients must be CUDA tensors")
     with _on_device(index):
-        if not _alike(grads, None, index):
+        if not _plain(grads, None, index):
             for g in grads:
                 if g.get_device() != index or g.layout != torch.strided:
                     raise RKLError(2, "gradients must be dense tensors on one device")
@@ -200,9 +208,11 @@ class AdamW:
             raise RKLError(2, "norm must be a 1-element float32 tensor beside the parameters")
         index = device.index
         with _on_device(index):
-            if any(g is None for g in grads) or not _alike(grads, self._shapes, index):
+            if _plain(grads, self._shapes, index):
+                ptrs = array("Q", [g.data_ptr() for g in grads])
+            else:
                 grads = self._each_checked(grads, index)
-            ptrs = array("Q", [0 if g is None else g.data_ptr() for g in grads])
+                ptrs = array("Q", [0 if g is None else g.data_ptr() for g in grads])
             codes = _dtype_codes(grads, "gradient")
             if max_norm is not None and norm is None:
                 norm = _norm_into(n, ptrs, self._numel, codes, device)
