@@ -1410,17 +1410,19 @@ struct FfnPlan {
   bool tc = false, skinny = false;     // sizes for the tensor cores; few rows
   SkinnyPlan up, down;
   int parts = 1, part_rows = 0;        // of y (forward) or dx (backward)
+  bool wide_planes = true;             // a, dg, du in fp32
   size_t plane = 0;                    // bytes of a [T, F] operand
   size_t off_counter = 0, off_part = 0, total = 0;
 };
 
 static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, bool backward) {
   FfnPlan p;
-  p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 : 4);
+  p.tc = dtype == RKL_BF16 && H % 8 == 0 && F % 8 == 0 && O % 8 == 0 && T > 0;
+  p.wide_planes = !p.tc;
+  p.plane = size_t(T) * F * (p.wide_planes ? 4 : 2);
   p.off_counter = align256((backward ? 3 : 1) * p.plane);
   p.off_part = p.off_counter + 256;
   p.total = p.off_part;
-  p.tc = dtype == RKL_BF16 && H % 8 == 0 && F % 8 == 0 && O % 8 == 0 && T > 0;
   if (!p.tc) return p;
   p.part_rows = static_cast<int>((T + 31) / 32 * 32);
   if (backward) {
@@ -1629,11 +1631,13 @@ rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up, 
   a.n = 1;
   a.act = activation;
   a.saved = saved;
+  a.wide_planes = plan.wide_planes;
+  const bool wide = plan.wide_planes;
   // a = act(x Wg^T) (x Wu^T)
-  a.p[0] = {{x, nullptr}, {W_gate, W_up}, workspace, T, F, H, H, 1, 1, H, 1, 0};
+  a.p[0] = {{x, nullptr}, {W_gate, W_up}, workspace, T, F, H, H, 1, 1, H, 1, 0, false, false};
   RKL_CUDA(launch_ffn_simt(FFN_UP, bf16, a, sms, s));
   // y = a Wd^T
-  a.p[0] = {{workspace, nullptr}, {W_down, nullptr}, y, T, O, F, F, 1, 1, F, 1, 0};
+  a.p[0] = {{workspace, nullptr}, {W_down, nullptr}, y, T, O, F, F, 1, 1, F, 1, 0, wide, false};
   RKL_CUDA(launch_ffn_simt(FFN_GEMM, bf16, a, sms, s));
   return RKL_OK;
 }
@@ -1678,17 +1682,19 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
   a.act = activation;
   a.saved = const_cast<float*>(saved);
   uint8_t* act = static_cast<uint8_t*>(workspace);  // a, dg and du, [T, F] each
-  const uint8_t* dg = act + size_t(T) * F * es;
-  const uint8_t* du = dg + size_t(T) * F * es;
+  const uint8_t* dg = act + plan.plane;
+  const uint8_t* du = dg + plan.plane;
+  const bool wide = plan.wide_planes;
+  a.wide_planes = wide;
   // da = dy Wd -> a, dg, du
   a.n = 1;
-  a.p[0] = {{dy, nullptr}, {W_down, nullptr}, act, T, F, O, O, 1, F, 1, 1, 0};
+  a.p[0] = {{dy, nullptr}, {W_down, nullptr}, act, T, F, O, O, 1, F, 1, 1, 0, false, false};
   RKL_CUDA(launch_ffn_simt(FFN_DGATE, bf16, a, sms, s));
   a.n = 0;
-  if (dx) a.p[a.n++] = {{dg, du}, {W_gate, W_up}, dx, T, H, F, F, 1, H, 1, 2, 0};
-  if (dW_gate) a.p[a.n++] = {{dg, nullptr}, {x, nullptr}, dW_gate, F, H, T, 1, F, H, 1, 1, 0};
-  if (dW_up) a.p[a.n++] = {{du, nullptr}, {x, nullptr}, dW_up, F, H, T, 1, F, H, 1, 1, 0};
-  if (dW_down) a.p[a.n++] = {{dy, nullptr}, {act, nullptr}, dW_down, O, F, T, 1, O, F, 1, 1, 0};
+  if (dx) a.p[a.n++] = {{dg, du}, {W_gate, W_up}, dx, T, H, F, F, 1, H, 1, 2, 0, wide, false};
+  if (dW_gate) a.p[a.n++] = {{dg, nullptr}, {x, nullptr}, dW_gate, F, H, T, 1, F, H, 1, 1, 0, wide, false};
+  if (dW_up) a.p[a.n++] = {{du, nullptr}, {x, nullptr}, dW_up, F, H, T, 1, F, H, 1, 1, 0, wide, false};
+  if (dW_down) a.p[a.n++] = {{dy, nullptr}, {act, nullptr}, dW_down, O, F, T, 1, O, F, 1, 1, 0, false, wide};
   RKL_CUDA(launch_ffn_simt(FFN_GEMM, bf16, a, sms, s));
   return RKL_OK;
 }

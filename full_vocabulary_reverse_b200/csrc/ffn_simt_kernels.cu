@@ -1,6 +1,7 @@
 // ffn_simt_kernels.cu -- the gated feed-forward block on the CUDA cores: fp32
 // (tcgen05 has no fp32 input kind), and bf16 whose sizes or addresses the
-// tensor-core path's 16-byte TMA rows rule out.
+// tensor-core path's 16-byte TMA rows rule out.  Where the sizes lead here, a, dg
+// and du stay fp32 in bf16 problems too: nothing but the results is rounded.
 //
 //   g = x Wg^T, u = x Wu^T, a = act(g) u, y = a Wd^T
 //   da = dy Wd, dg = da u act'(g), du = da act(g)
@@ -75,65 +76,70 @@ __device__ __forceinline__ void slice_place(bool k_fast, int i, int* mn, int* k)
 // This thread's share of an operand's slices: position `mn` of the tile is row
 // mn0 + mn of p, or from position `half` on (half > 0) row mn0 + mn - half of
 // p2; rows at mn_end and behind are zero.  Element i of a slice lies offset[i]
-// elements behind the slice's start.
-template <typename T, int BT>
+// bytes behind the slice's start.
+template <int BT>
 struct Operand {
-  const T *p, *p2;  // at (mn0, first k of the next slice)
-  long long s_k;
+  const char *p, *p2;  // at (mn0, first k of the next slice)
+  long long advance_by;
   int offset[kShare<BT>];
   uint32_t rows, upper;  // bits: the element's row is there; it comes from p2
-  bool k_fast;
+  bool k_fast, wide;     // wide: fp32 elements, else bf16
 
-  __device__ __forceinline__ Operand(const void* base, const void* base2, long long s_mn, long long stride_k,
+  __device__ __forceinline__ Operand(const void* base, const void* base2, bool wide_, long long s_mn, long long s_k,
                                      long long mn0, long long mn_end, int half)
-      : p(static_cast<const T*>(base) + mn0 * s_mn), p2(static_cast<const T*>(base2) + (half > 0 ? mn0 * s_mn : 0)),
-        s_k(stride_k), rows(0), upper(0), k_fast(stride_k == 1) {
+      : rows(0), upper(0), k_fast(s_k == 1), wide(wide_) {
+    const int size = wide ? 4 : 2;
+    p = static_cast<const char*>(base) + mn0 * s_mn * size;
+    p2 = half > 0 ? static_cast<const char*>(base2) + mn0 * s_mn * size : nullptr;
+    advance_by = kDepth<BT> * s_k * size;
 #pragma unroll
     for (int i = 0; i < kShare<BT>; ++i) {
       int mn, k;
       slice_place<BT>(k_fast, i, &mn, &k);
       const bool second = half > 0 && mn >= half;
       const int row = second ? mn - half : mn;
-      offset[i] = static_cast<int>(row * s_mn + k * s_k);  // strides are below 2^20: it fits
+      offset[i] = static_cast<int>(row * s_mn + k * s_k) * size;  // strides are at most 2^20, one of them 1: it fits
       rows |= (mn0 + row < mn_end ? 1u : 0u) << i;
       upper |= (second ? 1u : 0u) << i;
     }
   }
   // element i of the slice with `left` positions along k; *k: its place there
-  __device__ __forceinline__ const T* at(int i, int left, int* mn, int* k, bool* in) const {
+  __device__ __forceinline__ const char* at(int i, int left, int* mn, int* k, bool* in) const {
     slice_place<BT>(k_fast, i, mn, k);
     *in = ((rows >> i) & 1) && *k < left;
     return ((upper >> i) & 1 ? p2 : p) + offset[i];
   }
   __device__ __forceinline__ void advance() {
-    p += kDepth<BT> * s_k;
-    p2 += kDepth<BT> * s_k;
+    p += advance_by;
+    p2 += advance_by;
   }
 };
 
 // fp32: straight into shared memory, 4 bytes at a time (rows need no
 // alignment), zeros where nothing is read.
 template <int BT>
-__device__ __forceinline__ void slice_async(const Operand<float, BT>& o, int left, float (*s)[BT + 4]) {
+__device__ __forceinline__ void slice_async(const Operand<BT>& o, int left, float (*s)[BT + 4]) {
 #pragma unroll
   for (int i = 0; i < kShare<BT>; ++i) {
     int mn, k;
     bool in;
-    const float* p = o.at(i, left, &mn, &k, &in);
+    const char* p = o.at(i, left, &mn, &k, &in);
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][mn]));
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in ? p : o.p), "r"(in ? 4 : 0) : "memory");
   }
 }
 
-// bf16: through registers, widened to fp32.
+// bf16 problems: through registers, widened to fp32.
 template <int BT>
-__device__ __forceinline__ void slice_load(const Operand<__nv_bfloat16, BT>& o, int left, float* v) {
+__device__ __forceinline__ void slice_load(const Operand<BT>& o, int left, float* v) {
 #pragma unroll
   for (int i = 0; i < kShare<BT>; ++i) {
     int mn, k;
     bool in;
-    const __nv_bfloat16* p = o.at(i, left, &mn, &k, &in);
-    v[i] = in ? __bfloat162float(*p) : 0.f;
+    const char* p = o.at(i, left, &mn, &k, &in);
+    v[i] = 0.f;
+    if (in)
+      v[i] = o.wide ? *reinterpret_cast<const float*>(p) : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
   }
 }
 template <int BT>
@@ -151,10 +157,15 @@ template <typename T, int MODE>
 __device__ __forceinline__ void finish(const FfnSimtArgs& a, const FfnProduct& p, long long m, long long n, float sum,
                                        float u) {
   const long long at = m * p.N + n;
-  T* c = static_cast<T*>(p.c) + at;
   float slope;
+  auto put_plane = [&](long long i, float x) {  // a, dg or du
+    if (sizeof(T) == 4 || a.wide_planes)
+      static_cast<float*>(p.c)[i] = x;
+    else
+      put(static_cast<T*>(p.c) + i, x);
+  };
   if (MODE == FFN_UP) {
-    put(c, act_of(a.act, sum, &slope) * u);
+    put_plane(at, act_of(a.act, sum, &slope) * u);
     if (a.saved != nullptr) {
       const long long sv = ffn_saved_at(m, n, p.N);
       a.saved[sv] = sum;
@@ -164,11 +175,11 @@ __device__ __forceinline__ void finish(const FfnSimtArgs& a, const FfnProduct& p
     const long long sv = ffn_saved_at(m, n, p.N), one = p.M * p.N;
     const float g = a.saved[sv], up = a.saved[ffn_saved_plane(p.M, p.N) + sv];
     const float h = act_of(a.act, g, &slope);
-    put(c, h * up);                      // a
-    put(c + one, sum * up * slope);      // dg
-    put(c + 2 * one, sum * h);           // du
+    put_plane(at, h * up);                  // a
+    put_plane(at + one, sum * up * slope);  // dg
+    put_plane(at + 2 * one, sum * h);       // du
   } else {
-    put(c, sum);
+    put(static_cast<T*>(p.c) + at, sum);
   }
 }
 
@@ -200,8 +211,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < R / 2; ++j) acc2[i][j] = 0;
 
-  Operand<T, BT> oa(p.a[0], nullptr, p.sam, p.sak, m0, p.M, 0);
-  Operand<T, BT> ob(p.b[0], p.b[1], p.sbn, p.sbk, n0, p.N, MODE == FFN_UP ? BN : 0);
+  Operand<BT> oa(p.a[0], nullptr, kAsync || p.a_wide, p.sam, p.sak, m0, p.M, 0);
+  Operand<BT> ob(p.b[0], p.b[1], kAsync || p.b_wide, p.sbn, p.sbk, n0, p.N, MODE == FFN_UP ? BN : 0);
   // Slices of all segments of K, one behind another; the loads run ahead.
   const int per_segment = static_cast<int>((p.K + kDepth<BT> - 1) / kDepth<BT>);
   const int slices = per_segment * p.segments;
@@ -214,8 +225,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
     ob.advance();
     if (ahead == per_segment && p.segments == 2) {
       left = static_cast<int>(p.K);
-      oa.p = static_cast<const T*>(p.a[1]) + m0 * p.sam;
-      ob.p = static_cast<const T*>(p.b[1]) + n0 * p.sbn;
+      oa.p = static_cast<const char*>(p.a[1]) + m0 * p.sam * (oa.wide ? 4 : 2);
+      ob.p = static_cast<const char*>(p.b[1]) + n0 * p.sbn * (ob.wide ? 4 : 2);
     }
   };
   auto multiply = [&](int slot) {

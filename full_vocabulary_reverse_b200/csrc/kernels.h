@@ -342,18 +342,21 @@ __device__ __forceinline__ long long ffn_saved_at(long long row, long long col, 
 #endif
 // C(m, n) = sum over segments and k of A_s(m, k) B_s(k, n), row-major C [M, N].
 // FFN_UP: b[0] and b[1] are the gate and up weights, c = act(g) u.
-// FFN_DGATE: c receives a, dg and du, [3][M, N].
+// FFN_DGATE: c receives a, dg and du, [3][M, N].  a, dg and du are of the
+// problem's type, or fp32 (FfnSimtArgs::wide_planes).
 struct FfnProduct {
   const void *a[2], *b[2];
   void* c;
   long long M, N, K, sam, sak, sbk, sbn;  // strides in elements; sak or sam is 1, sbk or sbn is 1
   int segments, first_tile;
+  bool a_wide, b_wide;  // fp32 operand of a bf16 problem (a, dg, du)
 };
 constexpr int kFfnProducts = 4;
 struct FfnSimtArgs {
   FfnProduct p[kFfnProducts];
   float* saved;  // g and u (FFN_UP: nullable)
   int n, act;
+  bool wide_planes;  // a, dg and du are fp32
 };
 cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s);
 

@@ -431,9 +431,10 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
  * O multiples of 8, 16-byte aligned tensors) runs on the tensor cores, the rest
  * on the CUDA cores.  T = 0 is allowed (x, y, dy, dx and saved may be NULL).
  *
- * Products accumulate in fp32; g, u, act and its derivative are fp32.  a, and
- * in the backward pass a, dg and du, are rounded once to dtype as operands of
- * the next product.
+ * Products accumulate in fp32; g, u, act and its derivative are fp32.  On the
+ * tensor cores a, and in the backward pass a, dg and du, are rounded once to
+ * dtype as operands of the next product; sizes that lead to the CUDA cores keep
+ * them in fp32.
  *
  * saved: g and u for the backward pass, fp32, rkl_ffn_saved_size elements in an
  * order of the library's own (NULL in the forward pass alone: not stored).  The
