@@ -63,7 +63,7 @@ static const char* const kKernelNames[K_COUNT] = {
     "count_teachers", "build_slots", "topk_fwd", "topk_bwd", "zw_dual_tc", "dz_topk_tc", "topk_rowk",
     "zw_single_tc", "dz_topk_single_tc", "adamw", "adamw8", "norm_partial", "norm_final",
     "ffn_up_simt", "ffn_dgate_simt", "ffn_gemm_simt", "ffn_up_tc", "ffn_dgate_tc", "ffn_gemm_tc", "ffn_skinny_tc",
-    "ffn_join"};
+    "ffn_join", "ffn_pad"};
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_COUNT) ? kKernelNames[id] : nullptr; }
 
@@ -1345,16 +1345,20 @@ static rkl_status check_ffn(rkl_dtype dtype, int activation, int64_t T, int64_t 
   return RKL_OK;
 }
 
-// The gated block's tensors are aligned to their elements.
-static rkl_status check_ffn_ptr(const void* p, const char* name, rkl_dtype dtype, bool required = true) {
+// fp32 tensors are aligned to their elements; so are bf16 ones of odd widths,
+// which are copied; TMA reads the others where they lie.
+static unsigned ffn_alignment(rkl_dtype dtype, int64_t H, int64_t F, int64_t O) {
+  return dtype == RKL_FP32 ? 4 : (H % 8 || F % 8 || O % 8) ? 2 : 16;
+}
+
+static rkl_status check_ffn_ptr(const void* p, const char* name, unsigned alignment, bool required = true) {
   if (p == nullptr) return required ? fail(RKL_ERR_NULL, "%s is NULL", name) : RKL_OK;
-  if (reinterpret_cast<uintptr_t>(p) & (dtype == RKL_BF16 ? 1 : 3))
-    return fail(RKL_ERR_ALIGN, "%s is not aligned to its elements", name);
+  if (reinterpret_cast<uintptr_t>(p) & (alignment - 1))
+    return fail(RKL_ERR_ALIGN, "%s is not %u-byte aligned", name, alignment);
   return RKL_OK;
 }
 
-// ---- plan of the gated block: sizes alone decide the layout, so that the
-// workspace that is asked for fits whichever path the addresses allow.
+// ---- plan of the gated block, by its sizes and type alone
 constexpr int kPlanSms = 148;
 
 // ffn_skinny_kernel's share: `per` steps a CTA (4 at least: a part is written
@@ -1407,19 +1411,30 @@ static int pair_parts(int64_t tiles, int64_t steps, int64_t others, int64_t M, i
 static int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 struct FfnPlan {
-  bool tc = false, skinny = false;     // sizes for the tensor cores; few rows
+  bool tc = false, skinny = false;     // on the tensor cores (bf16); few rows
   SkinnyPlan up, down;
   int parts = 1, part_rows = 0;        // of y (forward) or dx (backward)
-  bool wide_planes = true;             // a, dg, du in fp32
   size_t plane = 0;                    // bytes of a [T, F] operand
   size_t off_counter = 0, off_part = 0, total = 0;
+  bool padded = false;                 // bf16 of odd widths: copies at off_pad
+  size_t off_pad = 0;
 };
 
 static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, bool backward) {
   FfnPlan p;
-  p.tc = dtype == RKL_BF16 && H % 8 == 0 && F % 8 == 0 && O % 8 == 0 && T > 0;
-  p.wide_planes = !p.tc;
-  p.plane = size_t(T) * F * (p.wide_planes ? 4 : 2);
+  p.tc = dtype == RKL_BF16 && T > 0;
+  if (p.tc && (H % 8 || F % 8 || O % 8)) {
+    // rows of whole 16 bytes: the padded problem's plan, and copies behind its workspace
+    const int64_t Hp = (H + 7) / 8 * 8, Fp = (F + 7) / 8 * 8, Op = (O + 7) / 8 * 8;
+    p = ffn_plan(dtype, T, Hp, Fp, Op, backward);
+    p.padded = true;
+    p.off_pad = align256(p.total);
+    const size_t x = align256(T * Hp * 2), wide = align256(Fp * Hp * 2), down = align256(Op * Fp * 2),
+                 y = align256(T * Op * 2);
+    p.total = p.off_pad + (backward ? 2 * (x + 2 * wide + down) + y : x + 2 * wide + down + y);
+    return p;
+  }
+  p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 : 4);
   p.off_counter = align256((backward ? 3 : 1) * p.plane);
   p.off_part = p.off_counter + 256;
   p.total = p.off_part;
@@ -1589,6 +1604,42 @@ static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W
   return dx && p.parts > 1 ? join_pair(p, part, dx, T, H, s) : RKL_OK;
 }
 
+// The odd-width problem's matrices in rows of whole 16 bytes.
+struct Padding {
+  FfnPadArgs in = {}, out = {};
+  uint8_t* at;
+
+  explicit Padding(uint8_t* ws) : at(ws) {}
+  static int up8(int64_t n) { return static_cast<int>((n + 7) / 8 * 8); }
+  uint16_t* take(int64_t rows, int64_t cols) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(at);
+    at += align256(size_t(rows) * cols * 2);
+    return p;
+  }
+  static void add(FfnPadArgs& a, const void* src, void* dst, int64_t rows, int64_t cols, int64_t src_pitch,
+                  int64_t dst_rows, int64_t dst_cols) {
+    a.item[a.n++] = {static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), static_cast<int>(rows),
+                     static_cast<int>(cols),            static_cast<int>(src_pitch), static_cast<int>(dst_rows),
+                     static_cast<int>(dst_cols),        a.total};
+    a.total += dst_rows * dst_cols;
+  }
+  // A copy of an input, its rows padded too where they are an odd width elsewhere.
+  const void* input(const void* src, int64_t rows, int64_t cols, bool pad_rows) {
+    const int64_t r = pad_rows ? up8(rows) : rows, c = up8(cols);
+    uint16_t* p = take(r, c);
+    add(in, src, p, rows, cols, cols, r, c);
+    return p;
+  }
+  // Where an output is computed; `finish` copies it to dst (nullptr: left out).
+  void* output(void* dst, int64_t rows, int64_t cols, bool pad_rows) {
+    if (dst == nullptr) return nullptr;
+    const int64_t r = pad_rows ? up8(rows) : rows, c = up8(cols);
+    uint16_t* p = take(r, c);
+    add(out, p, dst, rows, cols, c, rows, cols);
+    return p;
+  }
+};
+
 rkl_status rkl_ffn_workspace_size(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, int32_t backward,
                                   size_t* bytes) {
   if (bytes == nullptr) return fail(RKL_ERR_NULL, "bytes is NULL");
@@ -1609,12 +1660,13 @@ rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up, 
                            void* workspace, size_t workspace_bytes, void* stream) {
   RKL_NVTX_RANGE();
   RKL_TRY(check_ffn(dtype, activation, T, H, F, O));
-  RKL_TRY(check_ffn_ptr(W_gate, "W_gate", dtype));
-  RKL_TRY(check_ffn_ptr(W_up, "W_up", dtype));
-  RKL_TRY(check_ffn_ptr(W_down, "W_down", dtype));
+  const unsigned align = ffn_alignment(dtype, H, F, O);
+  RKL_TRY(check_ffn_ptr(W_gate, "W_gate", align));
+  RKL_TRY(check_ffn_ptr(W_up, "W_up", align));
+  RKL_TRY(check_ffn_ptr(W_down, "W_down", align));
   if (T == 0) return RKL_OK;
-  RKL_TRY(check_ffn_ptr(x, "x", dtype));
-  RKL_TRY(check_ffn_ptr(y, "y", dtype));
+  RKL_TRY(check_ffn_ptr(x, "x", align));
+  RKL_TRY(check_ffn_ptr(y, "y", align));
   RKL_TRY(check_ptr(saved, "saved", false));
   const FfnPlan plan = ffn_plan(dtype, T, H, F, O, false);
   if (workspace == nullptr || workspace_bytes < plan.total)
@@ -1623,22 +1675,33 @@ rkl_status rkl_ffn_forward(const void* x, const void* W_gate, const void* W_up, 
   int sms = 0;
   RKL_TRY(device_setup(&sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool bf16 = dtype == RKL_BF16;
-  if (plan.tc && aligned16(x) && aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(y))
-    return ffn_forward_tc(plan, x, W_gate, W_up, W_down, activation, T, H, F, O, y, saved,
-                          static_cast<uint8_t*>(workspace), sms, s);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (plan.padded) {
+    Padding pad(ws + plan.off_pad);
+    const void* px = pad.input(x, T, H, false);
+    const void* pg = pad.input(W_gate, F, H, true);
+    const void* pu = pad.input(W_up, F, H, true);
+    const void* pd = pad.input(W_down, O, F, true);
+    void* py = pad.output(y, T, O, false);
+    RKL_CUDA(launch_ffn_pad(pad.in, s));
+    RKL_TRY(ffn_forward_tc(plan, px, pg, pu, pd, activation, T, Padding::up8(H), Padding::up8(F), Padding::up8(O), py,
+                           saved, ws, sms, s));
+    RKL_CUDA(launch_ffn_pad(pad.out, s));
+    return RKL_OK;
+  }
+  if (plan.tc) return ffn_forward_tc(plan, x, W_gate, W_up, W_down, activation, T, H, F, O, y, saved, ws, sms, s);
+  const auto f32 = [](const void* p) { return static_cast<const float*>(p); };
+  float* act = reinterpret_cast<float*>(ws);
   FfnSimtArgs a = {};
   a.n = 1;
   a.act = activation;
   a.saved = saved;
-  a.wide_planes = plan.wide_planes;
-  const bool wide = plan.wide_planes;
   // a = act(x Wg^T) (x Wu^T)
-  a.p[0] = {{x, nullptr}, {W_gate, W_up}, workspace, T, F, H, H, 1, 1, H, 1, 0, false, false};
-  RKL_CUDA(launch_ffn_simt(FFN_UP, bf16, a, sms, s));
+  a.p[0] = {{f32(x), nullptr}, {f32(W_gate), f32(W_up)}, act, T, F, H, H, 1, 1, H, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_UP, a, sms, s));
   // y = a Wd^T
-  a.p[0] = {{workspace, nullptr}, {W_down, nullptr}, y, T, O, F, F, 1, 1, F, 1, 0, wide, false};
-  RKL_CUDA(launch_ffn_simt(FFN_GEMM, bf16, a, sms, s));
+  a.p[0] = {{act, nullptr}, {f32(W_down), nullptr}, static_cast<float*>(y), T, O, F, F, 1, 1, F, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_GEMM, a, sms, s));
   return RKL_OK;
 }
 
@@ -1648,24 +1711,24 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
                             size_t workspace_bytes, void* stream) {
   RKL_NVTX_RANGE();
   RKL_TRY(check_ffn(dtype, activation, T, H, F, O));
-  RKL_TRY(check_ffn_ptr(W_gate, "W_gate", dtype));
-  RKL_TRY(check_ffn_ptr(W_up, "W_up", dtype));
-  RKL_TRY(check_ffn_ptr(W_down, "W_down", dtype));
-  RKL_TRY(check_ffn_ptr(dx, "dx", dtype, false));
-  RKL_TRY(check_ffn_ptr(dW_gate, "dW_gate", dtype, false));
-  RKL_TRY(check_ffn_ptr(dW_up, "dW_up", dtype, false));
-  RKL_TRY(check_ffn_ptr(dW_down, "dW_down", dtype, false));
+  const unsigned align = ffn_alignment(dtype, H, F, O);
+  RKL_TRY(check_ffn_ptr(W_gate, "W_gate", align));
+  RKL_TRY(check_ffn_ptr(W_up, "W_up", align));
+  RKL_TRY(check_ffn_ptr(W_down, "W_down", align));
+  RKL_TRY(check_ffn_ptr(dx, "dx", align, false));
+  RKL_TRY(check_ffn_ptr(dW_gate, "dW_gate", align, false));
+  RKL_TRY(check_ffn_ptr(dW_up, "dW_up", align, false));
+  RKL_TRY(check_ffn_ptr(dW_down, "dW_down", align, false));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool bf16 = dtype == RKL_BF16;
-  const size_t es = bf16 ? 2 : 4;
+  const size_t es = dtype == RKL_BF16 ? 2 : 4;
   if (T == 0) {  // no rows: the weights' gradients are zero
     if (dW_gate) RKL_CUDA(cudaMemsetAsync(dW_gate, 0, size_t(F) * H * es, s));
     if (dW_up) RKL_CUDA(cudaMemsetAsync(dW_up, 0, size_t(F) * H * es, s));
     if (dW_down) RKL_CUDA(cudaMemsetAsync(dW_down, 0, size_t(O) * F * es, s));
     return RKL_OK;
   }
-  RKL_TRY(check_ffn_ptr(x, "x", dtype));
-  RKL_TRY(check_ffn_ptr(dy, "dy", dtype));
+  RKL_TRY(check_ffn_ptr(x, "x", align));
+  RKL_TRY(check_ffn_ptr(dy, "dy", align));
   RKL_TRY(check_ptr(saved, "saved"));
   const FfnPlan plan = ffn_plan(dtype, T, H, F, O, true);
   if (workspace == nullptr || workspace_bytes < plan.total)
@@ -1674,28 +1737,44 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
   if (!dx && !dW_gate && !dW_up && !dW_down) return RKL_OK;
   int sms = 0;
   RKL_TRY(device_setup(&sms));
-  if (plan.tc && aligned16(x) && aligned16(W_gate) && aligned16(W_up) && aligned16(W_down) && aligned16(dy) &&
-      aligned16(dx) && aligned16(dW_gate) && aligned16(dW_up) && aligned16(dW_down))
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (plan.padded) {
+    Padding pad(ws + plan.off_pad);
+    const void* px = pad.input(x, T, H, false);
+    const void* pg = pad.input(W_gate, F, H, true);
+    const void* pu = pad.input(W_up, F, H, true);
+    const void* pd = pad.input(W_down, O, F, true);
+    const void* pdy = pad.input(dy, T, O, false);
+    void* pdx = pad.output(dx, T, H, false);
+    void* pdg = pad.output(dW_gate, F, H, true);
+    void* pdu = pad.output(dW_up, F, H, true);
+    void* pdd = pad.output(dW_down, O, F, true);
+    RKL_CUDA(launch_ffn_pad(pad.in, s));
+    RKL_TRY(ffn_backward_tc(plan, px, pg, pu, pd, activation, T, Padding::up8(H), Padding::up8(F), Padding::up8(O), pdy,
+                            saved, pdx, pdg, pdu, pdd, ws, sms, s));
+    RKL_CUDA(launch_ffn_pad(pad.out, s));
+    return RKL_OK;
+  }
+  if (plan.tc)
     return ffn_backward_tc(plan, x, W_gate, W_up, W_down, activation, T, H, F, O, dy, saved, dx, dW_gate, dW_up, dW_down,
-                           static_cast<uint8_t*>(workspace), sms, s);
+                           ws, sms, s);
+  const auto f32 = [](const void* p) { return static_cast<const float*>(p); };
+  const auto out = [](void* p) { return static_cast<float*>(p); };
   FfnSimtArgs a = {};
   a.act = activation;
   a.saved = const_cast<float*>(saved);
-  uint8_t* act = static_cast<uint8_t*>(workspace);  // a, dg and du, [T, F] each
-  const uint8_t* dg = act + plan.plane;
-  const uint8_t* du = dg + plan.plane;
-  const bool wide = plan.wide_planes;
-  a.wide_planes = wide;
+  float* act = reinterpret_cast<float*>(ws);  // a, dg and du, [T, F] each
+  const float *dg = act + T * F, *du = dg + T * F;
   // da = dy Wd -> a, dg, du
   a.n = 1;
-  a.p[0] = {{dy, nullptr}, {W_down, nullptr}, act, T, F, O, O, 1, F, 1, 1, 0, false, false};
-  RKL_CUDA(launch_ffn_simt(FFN_DGATE, bf16, a, sms, s));
+  a.p[0] = {{f32(dy), nullptr}, {f32(W_down), nullptr}, act, T, F, O, O, 1, F, 1, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_DGATE, a, sms, s));
   a.n = 0;
-  if (dx) a.p[a.n++] = {{dg, du}, {W_gate, W_up}, dx, T, H, F, F, 1, H, 1, 2, 0, wide, false};
-  if (dW_gate) a.p[a.n++] = {{dg, nullptr}, {x, nullptr}, dW_gate, F, H, T, 1, F, H, 1, 1, 0, wide, false};
-  if (dW_up) a.p[a.n++] = {{du, nullptr}, {x, nullptr}, dW_up, F, H, T, 1, F, H, 1, 1, 0, wide, false};
-  if (dW_down) a.p[a.n++] = {{dy, nullptr}, {act, nullptr}, dW_down, O, F, T, 1, O, F, 1, 1, 0, false, wide};
-  RKL_CUDA(launch_ffn_simt(FFN_GEMM, bf16, a, sms, s));
+  if (dx) a.p[a.n++] = {{dg, du}, {f32(W_gate), f32(W_up)}, out(dx), T, H, F, F, 1, H, 1, 2, 0};
+  if (dW_gate) a.p[a.n++] = {{dg, nullptr}, {f32(x), nullptr}, out(dW_gate), F, H, T, 1, F, H, 1, 1, 0};
+  if (dW_up) a.p[a.n++] = {{du, nullptr}, {f32(x), nullptr}, out(dW_up), F, H, T, 1, F, H, 1, 1, 0};
+  if (dW_down) a.p[a.n++] = {{f32(dy), nullptr}, {act, nullptr}, out(dW_down), O, F, T, 1, O, F, 1, 1, 0};
+  RKL_CUDA(launch_ffn_simt(FFN_GEMM, a, sms, s));
   return RKL_OK;
 }
 

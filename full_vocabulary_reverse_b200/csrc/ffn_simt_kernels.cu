@@ -1,7 +1,5 @@
-// ffn_simt_kernels.cu -- the gated feed-forward block on the CUDA cores: fp32
-// (tcgen05 has no fp32 input kind), and bf16 whose sizes or addresses the
-// tensor-core path's 16-byte TMA rows rule out.  Where the sizes lead here, a, dg
-// and du stay fp32 in bf16 problems too: nothing but the results is rounded.
+// ffn_simt_kernels.cu -- the gated feed-forward block in fp32 on the CUDA cores
+// (tcgen05 has no fp32 input kind).
 //
 //   g = x Wg^T, u = x Wu^T, a = act(g) u, y = a Wd^T
 //   da = dy Wd, dg = da u act'(g), du = da act(g)
@@ -21,10 +19,8 @@
 // where there are many tiles; else 64, whose 64 threads of results are four
 // times over, each for a quarter of every slice, and add up at the end: with
 // one tile an SM, 2 warps alone took twice as long.  fp32 forward and backward:
-// T = 509, H = O = 515, F = 1031 in 0.25 ms (19 TFLOP/s), T = 4096, H = O = 2048,
+// T = 509, H = O = 515, F = 1031 in 0.24 ms (20 TFLOP/s), T = 4096, H = O = 2048,
 // F = 4096 in 13.5 (46; a library's fp32 products run at 56).
-#include <cuda_bf16.h>
-
 #include "ffn_act.cuh"
 #include "kernels.h"
 
@@ -40,8 +36,6 @@ constexpr int kGroups = kSimtThreads / ((BT / kResults) * (BT / kResults));  // 
 template <int BT>
 constexpr int kShare = BT * kDepth<BT> / kSimtThreads;  // elements of an operand's slice that a thread moves
 
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 __device__ __forceinline__ float act_of(int act, float g, float* slope) {
   switch (act) {
@@ -76,96 +70,59 @@ __device__ __forceinline__ void slice_place(bool k_fast, int i, int* mn, int* k)
 // This thread's share of an operand's slices: position `mn` of the tile is row
 // mn0 + mn of p, or from position `half` on (half > 0) row mn0 + mn - half of
 // p2; rows at mn_end and behind are zero.  Element i of a slice lies offset[i]
-// bytes behind the slice's start.
+// elements behind the slice's start.
 template <int BT>
 struct Operand {
-  const char *p, *p2;  // at (mn0, first k of the next slice)
-  long long advance_by;
+  const float *p, *p2;  // at (mn0, first k of the next slice)
+  long long s_k;
   int offset[kShare<BT>];
   uint32_t rows, upper;  // bits: the element's row is there; it comes from p2
-  bool k_fast, wide;     // wide: fp32 elements, else bf16
+  bool k_fast;
 
-  __device__ __forceinline__ Operand(const void* base, const void* base2, bool wide_, long long s_mn, long long s_k,
+  __device__ __forceinline__ Operand(const float* base, const float* base2, long long s_mn, long long stride_k,
                                      long long mn0, long long mn_end, int half)
-      : rows(0), upper(0), k_fast(s_k == 1), wide(wide_) {
-    const int size = wide ? 4 : 2;
-    p = static_cast<const char*>(base) + mn0 * s_mn * size;
-    p2 = half > 0 ? static_cast<const char*>(base2) + mn0 * s_mn * size : nullptr;
-    advance_by = kDepth<BT> * s_k * size;
+      : p(base + mn0 * s_mn), p2(half > 0 ? base2 + mn0 * s_mn : nullptr), s_k(stride_k), rows(0), upper(0),
+        k_fast(stride_k == 1) {
 #pragma unroll
     for (int i = 0; i < kShare<BT>; ++i) {
       int mn, k;
       slice_place<BT>(k_fast, i, &mn, &k);
       const bool second = half > 0 && mn >= half;
       const int row = second ? mn - half : mn;
-      offset[i] = static_cast<int>(row * s_mn + k * s_k) * size;  // strides are at most 2^20, one of them 1: it fits
+      offset[i] = static_cast<int>(row * s_mn + k * s_k);  // strides are at most 2^20, one of them 1: it fits
       rows |= (mn0 + row < mn_end ? 1u : 0u) << i;
       upper |= (second ? 1u : 0u) << i;
     }
   }
-  // element i of the slice with `left` positions along k; *k: its place there
-  __device__ __forceinline__ const char* at(int i, int left, int* mn, int* k, bool* in) const {
-    slice_place<BT>(k_fast, i, mn, k);
-    *in = ((rows >> i) & 1) && *k < left;
-    return ((upper >> i) & 1 ? p2 : p) + offset[i];
-  }
   __device__ __forceinline__ void advance() {
-    p += advance_by;
-    p2 += advance_by;
+    p += kDepth<BT> * s_k;
+    p2 += kDepth<BT> * s_k;
+  }
+  // The slice with `left` positions along k, straight into shared memory, 4
+  // bytes at a time (rows need no alignment), zeros where nothing is read.
+  __device__ __forceinline__ void fetch(int left, float (*s)[BT + 4]) const {
+#pragma unroll
+    for (int i = 0; i < kShare<BT>; ++i) {
+      int mn, k;
+      slice_place<BT>(k_fast, i, &mn, &k);
+      const bool in = ((rows >> i) & 1) && k < left;
+      const float* from = ((upper >> i) & 1 ? p2 : p) + offset[i];
+      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][mn]));
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in ? from : p), "r"(in ? 4 : 0)
+                   : "memory");
+    }
   }
 };
 
-// fp32: straight into shared memory, 4 bytes at a time (rows need no
-// alignment), zeros where nothing is read.
-template <int BT>
-__device__ __forceinline__ void slice_async(const Operand<BT>& o, int left, float (*s)[BT + 4]) {
-#pragma unroll
-  for (int i = 0; i < kShare<BT>; ++i) {
-    int mn, k;
-    bool in;
-    const char* p = o.at(i, left, &mn, &k, &in);
-    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][mn]));
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in ? p : o.p), "r"(in ? 4 : 0) : "memory");
-  }
-}
-
-// bf16 problems: through registers, widened to fp32.
-template <int BT>
-__device__ __forceinline__ void slice_load(const Operand<BT>& o, int left, float* v) {
-#pragma unroll
-  for (int i = 0; i < kShare<BT>; ++i) {
-    int mn, k;
-    bool in;
-    const char* p = o.at(i, left, &mn, &k, &in);
-    v[i] = 0.f;
-    if (in)
-      v[i] = o.wide ? *reinterpret_cast<const float*>(p) : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
-  }
-}
-template <int BT>
-__device__ __forceinline__ void slice_store(bool k_fast, const float* v, float (*s)[BT + 4]) {
-#pragma unroll
-  for (int i = 0; i < kShare<BT>; ++i) {
-    int mn, k;
-    slice_place<BT>(k_fast, i, &mn, &k);
-    s[k][mn] = v[i];
-  }
-}
-
 // What element (m, n) goes through: its sum, and in the up form u's.
-template <typename T, int MODE>
+template <int MODE>
 __device__ __forceinline__ void finish(const FfnSimtArgs& a, const FfnProduct& p, long long m, long long n, float sum,
                                        float u) {
   const long long at = m * p.N + n;
+  float* c = p.c + at;
   float slope;
-  auto put_plane = [&](long long i, float x) {  // a, dg or du
-    if (sizeof(T) == 4 || a.wide_planes)
-      static_cast<float*>(p.c)[i] = x;
-    else
-      put(static_cast<T*>(p.c) + i, x);
-  };
   if (MODE == FFN_UP) {
-    put_plane(at, act_of(a.act, sum, &slope) * u);
+    *c = act_of(a.act, sum, &slope) * u;
     if (a.saved != nullptr) {
       const long long sv = ffn_saved_at(m, n, p.N);
       a.saved[sv] = sum;
@@ -175,22 +132,21 @@ __device__ __forceinline__ void finish(const FfnSimtArgs& a, const FfnProduct& p
     const long long sv = ffn_saved_at(m, n, p.N), one = p.M * p.N;
     const float g = a.saved[sv], up = a.saved[ffn_saved_plane(p.M, p.N) + sv];
     const float h = act_of(a.act, g, &slope);
-    put_plane(at, h * up);                  // a
-    put_plane(at + one, sum * up * slope);  // dg
-    put_plane(at + 2 * one, sum * h);       // du
+    *c = h * up;                   // a
+    c[one] = sum * up * slope;     // dg
+    c[2 * one] = sum * h;          // du
   } else {
-    put(static_cast<T*>(p.c) + at, sum);
+    *c = sum;
   }
 }
 
 }  // namespace
 
-template <typename T, int BT, int MODE>
+template <int BT, int MODE>
 __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_constant__ FfnSimtArgs a) {
   constexpr int R = kResults;
   constexpr int STEP = BT / 2;  // between a thread's groups of 4
   constexpr int BN = MODE == FFN_UP ? BT / 2 : BT;  // result columns of a tile
-  constexpr bool kAsync = sizeof(T) == 4;
   constexpr int RING = 2;  // one slice is multiplied, the next is on its way
   __shared__ __align__(16) float sa[RING][kDepth<BT>][BT + 4];
   __shared__ __align__(16) float sb[RING][kDepth<BT>][BT + 4];
@@ -211,8 +167,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < R / 2; ++j) acc2[i][j] = 0;
 
-  Operand<BT> oa(p.a[0], nullptr, kAsync || p.a_wide, p.sam, p.sak, m0, p.M, 0);
-  Operand<BT> ob(p.b[0], p.b[1], kAsync || p.b_wide, p.sbn, p.sbk, n0, p.N, MODE == FFN_UP ? BN : 0);
+  Operand<BT> oa(p.a[0], nullptr, p.sam, p.sak, m0, p.M, 0);
+  Operand<BT> ob(p.b[0], p.b[1], p.sbn, p.sbk, n0, p.N, MODE == FFN_UP ? BN : 0);
   // Slices of all segments of K, one behind another; the loads run ahead.
   const int per_segment = static_cast<int>((p.K + kDepth<BT> - 1) / kDepth<BT>);
   const int slices = per_segment * p.segments;
@@ -225,8 +181,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
     ob.advance();
     if (ahead == per_segment && p.segments == 2) {
       left = static_cast<int>(p.K);
-      oa.p = static_cast<const char*>(p.a[1]) + m0 * p.sam * (oa.wide ? 4 : 2);
-      ob.p = static_cast<const char*>(p.b[1]) + n0 * p.sbn * (ob.wide ? 4 : 2);
+      oa.p = p.a[1] + m0 * p.sam;
+      ob.p = p.b[1] + n0 * p.sbn;
     }
   };
   auto multiply = [&](int slot) {
@@ -252,38 +208,21 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
       }
     }
   };
-  if constexpr (kAsync) {
-    auto issue = [&] {  // (a group each time, an empty one at the end)
-      if (ahead < slices) {
-        slice_async<BT>(oa, left, sa[ahead % RING]);
-        slice_async<BT>(ob, left, sb[ahead % RING]);
-        advance();
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll 1
-    for (int i = 0; i < RING - 1; ++i) issue();
-    for (int s = 0; s < slices; ++s) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
-      __syncthreads();  // slice s is there for all; all are done with slice s - 1, whose slot the next load takes
-      issue();
-      multiply(s % RING);
-    }
-  } else {
-    float va[kShare<BT>], vb[kShare<BT>];
-    auto fetch = [&] {
-      slice_load<BT>(oa, left, va);
-      slice_load<BT>(ob, left, vb);
+  auto issue = [&] {  // (a group each time, an empty one at the end)
+    if (ahead < slices) {
+      oa.fetch(left, sa[ahead % RING]);
+      ob.fetch(left, sb[ahead % RING]);
       advance();
-    };
-    fetch();
-    for (int s = 0; s < slices; ++s) {
-      slice_store<BT>(p.sak == 1, va, sa[s % RING]);
-      slice_store<BT>(p.sbk == 1, vb, sb[s % RING]);
-      __syncthreads();  // (this slot's last readers are past an earlier barrier)
-      if (ahead < slices) fetch();
-      multiply(s % RING);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < RING - 1; ++i) issue();
+  for (int s = 0; s < slices; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
+    __syncthreads();  // slice s is there for all; all are done with slice s - 1, whose slot the next load takes
+    issue();
+    multiply(s % RING);
   }
 
   float acc[R][R];
@@ -331,7 +270,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
 #pragma unroll 4
     for (int e = threadIdx.x; e < BT * BN; e += kSimtThreads) {
       const int r = e / BN, c = e % BN;
-      if (m0 + r < p.M && n0 + c < p.N) finish<T, MODE>(a, p, m0 + r, n0 + c, whole[r][c], whole[r][(c + BN) % BT]);
+      if (m0 + r < p.M && n0 + c < p.N) finish<MODE>(a, p, m0 + r, n0 + c, whole[r][c], whole[r][(c + BN) % BT]);
     }
   } else {
 #pragma unroll
@@ -342,13 +281,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2) ffn_simt_kernel(const __grid_
       for (int j = 0; j < (MODE == FFN_UP ? 4 : R); ++j) {
         // up: a thread's first group of columns are gates, its second the ups of the same elements
         const long long n = n0 + tx * 4 + (j / 4) * STEP + j % 4;
-        if (n < p.N) finish<T, MODE>(a, p, m, n, acc[i][j], acc[i][(j + 4) % R]);
+        if (n < p.N) finish<MODE>(a, p, m, n, acc[i][j], acc[i][(j + 4) % R]);
       }
     }
   }
 }
 
-template <typename T, int BT>
+template <int BT>
 static cudaError_t launch_simt_bt(int mode, FfnSimtArgs& a, cudaStream_t s) {
   long long tiles = 0;
   for (int i = 0; i < a.n; ++i) {
@@ -361,24 +300,22 @@ static cudaError_t launch_simt_bt(int mode, FfnSimtArgs& a, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(tiles));
   LaunchScope scope(mode == FFN_UP ? K_FFN_UP_SIMT : mode == FFN_DGATE ? K_FFN_DGATE_SIMT : K_FFN_GEMM_SIMT, s);
   if (mode == FFN_UP)
-    ffn_simt_kernel<T, BT, FFN_UP><<<grid, kSimtThreads, 0, s>>>(a);
+    ffn_simt_kernel<BT, FFN_UP><<<grid, kSimtThreads, 0, s>>>(a);
   else if (mode == FFN_DGATE)
-    ffn_simt_kernel<T, BT, FFN_DGATE><<<grid, kSimtThreads, 0, s>>>(a);
+    ffn_simt_kernel<BT, FFN_DGATE><<<grid, kSimtThreads, 0, s>>>(a);
   else
-    ffn_simt_kernel<T, BT, FFN_GEMM><<<grid, kSimtThreads, 0, s>>>(a);
+    ffn_simt_kernel<BT, FFN_GEMM><<<grid, kSimtThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s) {
+cudaError_t launch_ffn_simt(int mode, FfnSimtArgs a, int sms, cudaStream_t s) {
   long long big = 0;
   for (int i = 0; i < a.n; ++i) big += (a.p[i].M + 127) / 128 * ((a.p[i].N + (mode == FFN_UP ? 63 : 127)) / (mode == FFN_UP ? 64 : 128));
   // 128-wide tiles do twice the work for each shared load, but take four times
   // as long each, one or two on an SM: they pay from some two waves on (T = 2000, H = O = 1024,
   // F = 2048: 2.06 ms forward and backward against 2.35).
   const bool wide = big >= 2 * sms;
-  if (bf16)
-    return wide ? launch_simt_bt<__nv_bfloat16, 128>(mode, a, s) : launch_simt_bt<__nv_bfloat16, 64>(mode, a, s);
-  return wide ? launch_simt_bt<float, 128>(mode, a, s) : launch_simt_bt<float, 64>(mode, a, s);
+  return wide ? launch_simt_bt<128>(mode, a, s) : launch_simt_bt<64>(mode, a, s);
 }
 
 }  // namespace rkl

@@ -50,6 +50,7 @@ enum KernelId : int {
   K_FFN_GEMM_TC,      // gated block, tcgen05: down projection, dx and weight gradients
   K_FFN_SKINNY_TC,    // gated block, tcgen05: projections of few rows (parts)
   K_FFN_JOIN,         // gated block: parts joined (with the activation after the first half)
+  K_FFN_PAD,          // gated block: matrices of odd widths to and from rows of whole 16 bytes
   K_COUNT
 };
 
@@ -342,23 +343,20 @@ __device__ __forceinline__ long long ffn_saved_at(long long row, long long col, 
 #endif
 // C(m, n) = sum over segments and k of A_s(m, k) B_s(k, n), row-major C [M, N].
 // FFN_UP: b[0] and b[1] are the gate and up weights, c = act(g) u.
-// FFN_DGATE: c receives a, dg and du, [3][M, N].  a, dg and du are of the
-// problem's type, or fp32 (FfnSimtArgs::wide_planes).
+// FFN_DGATE: c receives a, dg and du, [3][M, N].
 struct FfnProduct {
-  const void *a[2], *b[2];
-  void* c;
+  const float *a[2], *b[2];
+  float* c;
   long long M, N, K, sam, sak, sbk, sbn;  // strides in elements; sak or sam is 1, sbk or sbn is 1
   int segments, first_tile;
-  bool a_wide, b_wide;  // fp32 operand of a bf16 problem (a, dg, du)
 };
 constexpr int kFfnProducts = 4;
 struct FfnSimtArgs {
   FfnProduct p[kFfnProducts];
   float* saved;  // g and u (FFN_UP: nullable)
   int n, act;
-  bool wide_planes;  // a, dg and du are fp32
 };
-cudaError_t launch_ffn_simt(int mode, bool bf16, FfnSimtArgs a, int sms, cudaStream_t s);
+cudaError_t launch_ffn_simt(int mode, FfnSimtArgs a, int sms, cudaStream_t s);
 
 // tcgen05 path (ffn_tc_kernels.cu).
 constexpr int kFfnSkinnyRows = 128;  // rows up to which the weights are the M operand
@@ -398,6 +396,21 @@ struct FfnJoinArgs {
   long long per;           // > 0: parts as ffn_skinny_kernel numbers them; 0: `parts` everywhere
   int T, N, second, steps, parts;
 };
+// Copies bf16 matrices between layouts: dst (dst_rows x dst_cols, its pitch)
+// takes src (rows x cols at pitch src_pitch), zeros elsewhere.
+struct FfnPadItem {
+  const uint16_t* src;
+  uint16_t* dst;
+  int rows, cols, src_pitch, dst_rows, dst_cols;
+  long long first;         // elements of the items before this one
+};
+constexpr int kFfnPadItems = 5;
+struct FfnPadArgs {
+  FfnPadItem item[kFfnPadItems];
+  int n;
+  long long total;         // elements written
+};
+cudaError_t launch_ffn_pad(const FfnPadArgs& a, cudaStream_t s);
 cudaError_t ffn_tc_setup();
 cudaError_t launch_ffn_pair(int mode, int act, const FfnPairArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_ffn_skinny(FfnSkinnyArgs a, int grid, cudaStream_t s);

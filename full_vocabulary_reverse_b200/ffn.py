@@ -46,6 +46,12 @@ def _sizes(x, W_gate, W_up, W_down):
     return code, T, H, F, O
 
 
+def _ready(t):
+    """t, or a copy that is contiguous from a 16-byte boundary."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 @lru_cache(maxsize=1024)
 def _workspace_size(code, T, H, F, O, backward):
     nbytes = ctypes.c_size_t(0)
@@ -65,7 +71,7 @@ def ffn_forward(x, W_gate, W_up, W_down, activation=ACT_SILU, save=False):
     ``ffn_backward``) is None unless ``save``."""
     code, T, H, F, O = _sizes(x, W_gate, W_up, W_down)
     # (bound to names: a copy has to live until the call returns)
-    x, W_gate, W_up, W_down = x.contiguous(), W_gate.contiguous(), W_up.contiguous(), W_down.contiguous()
+    x, W_gate, W_up, W_down = _ready(x), _ready(W_gate), _ready(W_up), _ready(W_down)
     device = x.device
     with _on_device(device.index):
         y = torch.empty((T, O), dtype=x.dtype, device=device)
@@ -88,8 +94,7 @@ def ffn_backward(x, W_gate, W_up, W_down, dy, saved, activation=ACT_SILU, needs=
     if saved.shape != (_saved_size(T, F),) or saved.dtype != torch.float32 or saved.device != device \
             or not saved.is_contiguous():
         raise RKLError(2, "saved must be what ffn_forward gave for the same sizes")
-    x, W_gate, W_up, W_down = x.contiguous(), W_gate.contiguous(), W_up.contiguous(), W_down.contiguous()
-    dy = dy.contiguous()
+    x, W_gate, W_up, W_down, dy = _ready(x), _ready(W_gate), _ready(W_up), _ready(W_down), _ready(dy)
     with _on_device(device.index):
         out = [torch.empty_like(t) if need else None for t, need in zip((x, W_gate, W_up, W_down), needs)]
         nbytes = _workspace_size(code, T, H, F, O, 1)

@@ -427,14 +427,15 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
  *     g = x W_gate^T,  u = x W_up^T,  a = act(g) u,  y = a W_down^T
  *
  * x [T, H], W_gate and W_up [F, H], W_down [O, F], y [T, O]; all of one dtype,
- * contiguous, aligned to their elements.  Any sizes: bf16 on 16-byte rows (H, F,
- * O multiples of 8, 16-byte aligned tensors) runs on the tensor cores, the rest
- * on the CUDA cores.  T = 0 is allowed (x, y, dy, dx and saved may be NULL).
+ * contiguous.  Any sizes.  bf16 runs on the tensor cores: where H, F and O are
+ * multiples of 8 the tensors must be 16-byte aligned; otherwise they need only be
+ * aligned to their elements, and the call works on copies in rows of whole 16
+ * bytes (in the workspace).  fp32 runs on the CUDA cores, aligned to its elements.
+ * T = 0 is allowed (x, y, dy, dx and saved may be NULL).
  *
- * Products accumulate in fp32; g, u, act and its derivative are fp32.  On the
- * tensor cores a, and in the backward pass a, dg and du, are rounded once to
- * dtype as operands of the next product; sizes that lead to the CUDA cores keep
- * them in fp32.
+ * Products accumulate in fp32; g, u, act and its derivative are fp32.  a, and
+ * in the backward pass a, dg and du, are rounded once to dtype as operands of
+ * the next product.
  *
  * saved: g and u for the backward pass, fp32, rkl_ffn_saved_size elements in an
  * order of the library's own (NULL in the forward pass alone: not stored).  The

@@ -39,7 +39,8 @@ def backward(L, **kw):
 
 BOTH = [(dict(dtype=5), 3), (dict(act=4), 3), (dict(act=-1), 3), (dict(T=-1), 2), (dict(H=0), 2), (dict(F=0), 2),
         (dict(O=0), 2), (dict(T=1 << 31), 2), (dict(F=1 << 21), 2), (dict(x=0), 1), (dict(wg=0), 1), (dict(wu=0), 1),
-        (dict(wd=0), 1), (dict(x=GOOD + 1), 4), (dict(wg=GOOD + 2, dtype=1), 4), (dict(ws=0), 5), (dict(nbytes=64), 5),
+        (dict(wd=0), 1), (dict(x=GOOD + 1), 4), (dict(x=GOOD + 8), 4), (dict(wd=GOOD + 2), 4), (dict(wd=GOOD + 1, H=15), 4),
+        (dict(wg=GOOD + 2, dtype=1), 4), (dict(ws=0), 5), (dict(nbytes=64), 5),
         (dict(ws=GOOD + 4), 4), (dict(saved=GOOD + 4), 4)]
 
 

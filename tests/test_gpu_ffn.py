@@ -35,7 +35,7 @@ def both(T, H, F, O, dtype, kind, seed=0, scale=1.0):
 SIZES = [(1, 8, 8, 8), (1, 1, 1, 1), (1, 512, 1032, 264), (2, 64, 72, 40), (3, 65, 33, 17), (5, 1032, 200, 520),
          (8, 256, 2048, 256), (9, 264, 136, 8), (31, 200, 77, 64), (64, 128, 128, 128), (127, 96, 264, 72),
          (128, 256, 256, 256), (129, 136, 520, 328), (255, 64, 1000, 64), (257, 320, 264, 1032), (300, 515, 131, 67),
-         (513, 72, 88, 2056), (700, 1160, 344, 120)]
+         (513, 72, 88, 2056), (700, 1160, 344, 120), (1500, 349, 699, 351)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -157,9 +157,9 @@ def test_memory_behind_the_results_is_left_alone(T, H, F, O):
     assert torch.equal(out[0][rows], y[rows]) and torch.equal(out[1][rows], dx[rows])
 
 
-@pytest.mark.parametrize("T", [1, 20, 500])
-def test_captured_pass_and_other_stream(T):
-    ins, dy = inputs(T, 128, 264, 72, torch.bfloat16, 4)
+@pytest.mark.parametrize("T,H", [(1, 128), (20, 128), (500, 128), (20, 125), (500, 125)])
+def test_captured_pass_and_other_stream(T, H):
+    ins, dy = inputs(T, H, 264, 72, torch.bfloat16, 4)
     leaves = [t.requires_grad_(True) for t in ins]
 
     def step():
