@@ -36,7 +36,6 @@ constexpr int kGroups = kSimtThreads / ((BT / kResults) * (BT / kResults));  // 
 template <int BT>
 constexpr int kShare = BT * kDepth<BT> / kSimtThreads;  // elements of an operand's slice that a thread moves
 
-
 __device__ __forceinline__ float act_of(int act, float g, float* slope) {
   switch (act) {
     case ACT_SILU: return act_with_slope<ACT_SILU, false>(g, slope);
