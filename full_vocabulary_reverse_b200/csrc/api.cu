@@ -1412,11 +1412,12 @@ static int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 struct FfnPlan {
   bool tc = false, skinny = false;     // on the tensor cores (bf16); few rows
+  int terms = 1;                       // bf16 terms of a, dg and du
   SkinnyPlan up, down;
   int parts = 1, part_rows = 0;        // of y (forward) or dx (backward)
   size_t plane = 0;                    // bytes of a [T, F] operand
   size_t off_counter = 0, off_part = 0, total = 0;
-  bool padded = false;                 // bf16 of odd widths: copies at off_pad
+  bool padded = false;                 // bf16 of odd widths: copies at off_pad (backward, two terms: x and dy)
   size_t off_pad = 0;
 };
 
@@ -1431,28 +1432,33 @@ static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_
     p.off_pad = align256(p.total);
     const size_t x = align256(T * Hp * 2), wide = align256(Fp * Hp * 2), down = align256(Op * Fp * 2),
                  y = align256(T * Op * 2);
-    p.total = p.off_pad + (backward ? 2 * (x + 2 * wide + down) + y : x + 2 * wide + down + y);
+    p.total = p.off_pad + (backward ? p.terms * (x + y) + x + 2 * (2 * wide + down) : x + 2 * wide + down + y);
     return p;
   }
-  p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 : 4);
+  if (p.tc && T <= kFfnTermRows && (T * F <= kFfnTermElements || T * (H < O ? H : O) <= kFfnTermResults)) p.terms = 2;
+  p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 * p.terms : 4);
   p.off_counter = align256((backward ? 3 : 1) * p.plane);
   p.off_part = p.off_counter + 256;
   p.total = p.off_part;
   if (!p.tc) return p;
-  p.part_rows = static_cast<int>((T + 31) / 32 * 32);
+  p.part_rows = static_cast<int>((p.terms * T + 31) / 32 * 32);
   if (backward) {
     const int64_t mt = tiles_of(T, 256), steps_t = tiles_of(T, 128);
     const int64_t others =
         (2 * tiles_of(F, 256) * tiles_of(H, 256) + tiles_of(O, 256) * tiles_of(F, 256)) * steps_t;
-    p.parts = pair_parts(mt * tiles_of(H, 256), 2 * tiles_of(F, 128), others, T, H);
-    if (p.parts > 1) p.total += size_t(p.parts) * p.part_rows * H * 4;
+    p.parts = pair_parts(mt * tiles_of(H, 256), 2 * tiles_of(F, 128), others, p.terms * T, H);
+    if (p.parts > 1 || p.terms > 1) p.total += size_t(p.parts) * p.part_rows * H * 4;
+    if (p.terms > 1) {
+      p.off_pad = align256(p.total);
+      p.total = p.off_pad + align256(2 * T * H * 2) + align256(2 * T * O * 2);
+    }
     return p;
   }
   p.skinny = T <= kFfnSkinnyRows;
   if (p.skinny) {
     p.up = skinny_plan(F, F, H);
     p.down = skinny_plan(O, 0, F);
-    const size_t up = size_t(p.up.parts) * T * p.up.pitch * 4, down = size_t(p.down.parts) * T * p.down.pitch * 4;
+    const size_t up = size_t(p.up.parts) * T * p.up.pitch * 4, down = size_t(p.down.parts) * p.terms * T * p.down.pitch * 4;
     p.total += up > down ? up : down;
     return p;
   }
@@ -1475,7 +1481,8 @@ static rkl_status result_map(CUtensorMap* m, const void* p, int64_t rows, int64_
 // One product of a launch's list: A and B row-major as they lie, `*_mn` where K
 // is their row index.
 static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bool a_mn, const void* B, const void* B2,
-                               bool b_mn, void* C, int64_t M, int64_t N, int64_t K, bool up, int parts, int part_rows) {
+                               bool b_mn, void* C, int64_t M, int64_t N, int64_t K, bool up, int parts = 1,
+                               int part_rows = 0) {
   FfnPairProduct& p = a.p[a.n++];
   RKL_TRY(operand_map(&p.a[0], A, a_mn ? K : M, a_mn ? M : K, a_mn));
   p.a[1] = p.a[0];
@@ -1483,7 +1490,7 @@ static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bo
   RKL_TRY(operand_map(&p.b[0], B, b_mn ? K : N, b_mn ? N : K, b_mn));
   p.b[1] = p.b[0];
   if (B2) RKL_TRY(operand_map(&p.b[1], B2, b_mn ? K : N, b_mn ? N : K, b_mn));
-  if (parts > 1)
+  if (part_rows > 0)
     RKL_TRY(make_map(&p.c, C, true, N, int64_t(parts) * part_rows, N * 4, 32, 32));
   else
     RKL_TRY(result_map(&p.c, C, M, N));
@@ -1532,12 +1539,14 @@ static FfnJoinArgs join_args(const float* part, void* out, int64_t T, int64_t N)
   return j;
 }
 
-static rkl_status join_skinny(const SkinnyPlan& p, int act, const float* part, void* out, float* saved, int64_t T,
-                              int64_t N, cudaStream_t s) {
+static rkl_status join_skinny(const SkinnyPlan& p, int act, const float* part, void* out, void* rest, float* saved,
+                              int64_t T, int64_t N, int terms, cudaStream_t s) {
   FfnJoinArgs j = join_args(part, out, T, N);
+  j.rest = static_cast<uint16_t*>(rest);
   j.saved = saved;
+  j.terms = terms;
   j.pitch = p.pitch;
-  j.slab = T * p.pitch;
+  j.slab = (act < 0 ? terms : 1) * T * p.pitch;  // (two terms: as many rows more)
   j.per = p.per;
   j.second = p.tiles_first * 128;
   j.steps = p.steps;
@@ -1550,6 +1559,7 @@ static rkl_status join_pair(const FfnPlan& p, const float* part, void* out, int6
   j.pitch = N;
   j.slab = int64_t(p.part_rows) * N;
   j.parts = p.parts;
+  j.terms = p.terms;
   RKL_CUDA(launch_ffn_join(-1, j, s));
   return RKL_OK;
 }
@@ -1560,22 +1570,24 @@ static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   if (p.skinny) {
     RKL_TRY(skinny_product(p.up, x, W_gate, F, W_up, T, H, part, false, s));
-    RKL_TRY(join_skinny(p.up, act, part, ws, saved, T, F, s));
-    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, T, F, part, true, s));
-    return join_skinny(p.down, -1, part, y, nullptr, T, O, s);
+    RKL_TRY(join_skinny(p.up, act, part, ws, p.terms > 1 ? ws + p.plane / 2 : nullptr, saved, T, F, p.terms, s));
+    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, p.terms * T, F, part, true, s));
+    return join_skinny(p.down, -1, part, y, nullptr, nullptr, T, O, p.terms, s);
   }
   FfnPairArgs a = {};
-  RKL_TRY(pair_product(a, x, nullptr, false, W_gate, W_up, false, ws, T, F, H, true, 1, 0));
+  RKL_TRY(pair_product(a, x, nullptr, false, W_gate, W_up, false, ws, T, F, H, true));
   a.saved = saved;
   RKL_CUDA(launch_ffn_pair(FFN_UP, act, a, sms, s));
   FfnPairArgs d = {};
   d.follows = true;
   RKL_TRY(pair_product(d, ws, nullptr, false, W_down, nullptr, false, p.parts > 1 ? static_cast<void*>(part) : y, T, O, F,
-                       false, p.parts, p.part_rows));
+                       false, p.parts, p.parts > 1 ? p.part_rows : 0));
   RKL_CUDA(launch_ffn_pair(FFN_GEMM, act, d, sms, s));
   return p.parts > 1 ? join_pair(p, part, y, T, O, s) : RKL_OK;
 }
 
+// p.terms = 2: x and dy hold their T rows twice, for the weights' gradients of
+// the 2 T rows that a, dg and du then are.
 static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W_gate, const void* W_up,
                                   const void* W_down, int act, int64_t T, int64_t H, int64_t F, int64_t O,
                                   const void* dy, const float* saved, void* dx, void* dW_gate, void* dW_up,
@@ -1584,27 +1596,32 @@ static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W
   int* counter = reinterpret_cast<int*>(ws + p.off_counter);
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   FfnPairArgs a = {};
-  RKL_TRY(pair_product(a, dy, nullptr, false, W_down, nullptr, true, a_plane, T, F, O, false, 1, 0));
+  RKL_TRY(pair_product(a, dy, nullptr, false, W_down, nullptr, true, a_plane, T, F, O, false));
   RKL_TRY(result_map(&a.c2, dg, T, F));
   RKL_TRY(result_map(&a.c3, du, T, F));
+  if (p.terms > 1)
+    for (int i = 0; i < 3; ++i) RKL_TRY(result_map(&a.rest[i], ws + i * p.plane + p.plane / 2, T, F));
   a.saved = const_cast<float*>(saved);
   a.zero_counter = counter;
-  RKL_CUDA(launch_ffn_pair(FFN_DGATE, act, a, sms, s));
+  RKL_CUDA(launch_ffn_pair(p.terms > 1 ? FFN_DGATE_TERMS : FFN_DGATE, act, a, sms, s));
   // longest items (K = 2 F) first
   FfnPairArgs d = {};
   d.follows = true;
   d.counter = counter;
+  const int64_t rows = p.terms * T;
+  const bool joined = p.parts > 1 || p.terms > 1;
   if (dx)
-    RKL_TRY(pair_product(d, dg, du, false, W_gate, W_up, true, p.parts > 1 ? static_cast<void*>(part) : dx, T, H, F, false,
-                         p.parts, p.part_rows));
-  if (dW_gate) RKL_TRY(pair_product(d, dg, nullptr, true, x, nullptr, true, dW_gate, F, H, T, false, 1, 0));
-  if (dW_up) RKL_TRY(pair_product(d, du, nullptr, true, x, nullptr, true, dW_up, F, H, T, false, 1, 0));
-  if (dW_down) RKL_TRY(pair_product(d, dy, nullptr, true, a_plane, nullptr, true, dW_down, O, F, T, false, 1, 0));
+    RKL_TRY(pair_product(d, dg, du, false, W_gate, W_up, true, joined ? static_cast<void*>(part) : dx, rows, H, F, false,
+                         p.parts, joined ? p.part_rows : 0));
+  if (dW_gate) RKL_TRY(pair_product(d, dg, nullptr, true, x, nullptr, true, dW_gate, F, H, rows, false));
+  if (dW_up) RKL_TRY(pair_product(d, du, nullptr, true, x, nullptr, true, dW_up, F, H, rows, false));
+  if (dW_down) RKL_TRY(pair_product(d, dy, nullptr, true, a_plane, nullptr, true, dW_down, O, F, rows, false));
   RKL_CUDA(launch_ffn_pair(FFN_GEMM, act, d, sms, s));
-  return dx && p.parts > 1 ? join_pair(p, part, dx, T, H, s) : RKL_OK;
+  return dx && joined ? join_pair(p, part, dx, T, H, s) : RKL_OK;
 }
 
-// The odd-width problem's matrices in rows of whole 16 bytes.
+// Matrices laid out anew: the odd-width problem's in rows of whole 16 bytes, and
+// x and dy twice where a backward pass has two terms.
 struct Padding {
   FfnPadArgs in = {}, out = {};
   uint8_t* at;
@@ -1624,10 +1641,10 @@ struct Padding {
     a.total += dst_rows * dst_cols;
   }
   // A copy of an input, its rows padded too where they are an odd width elsewhere.
-  const void* input(const void* src, int64_t rows, int64_t cols, bool pad_rows) {
+  const void* input(const void* src, int64_t rows, int64_t cols, bool pad_rows, int times = 1) {
     const int64_t r = pad_rows ? up8(rows) : rows, c = up8(cols);
-    uint16_t* p = take(r, c);
-    add(in, src, p, rows, cols, cols, r, c);
+    uint16_t* p = take(times * r, c);
+    for (int i = 0; i < times; ++i) add(in, src, p + i * r * c, rows, cols, cols, r, c);
     return p;
   }
   // Where an output is computed; `finish` copies it to dst (nullptr: left out).
@@ -1740,11 +1757,11 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (plan.padded) {
     Padding pad(ws + plan.off_pad);
-    const void* px = pad.input(x, T, H, false);
+    const void* px = pad.input(x, T, H, false, plan.terms);
     const void* pg = pad.input(W_gate, F, H, true);
     const void* pu = pad.input(W_up, F, H, true);
     const void* pd = pad.input(W_down, O, F, true);
-    const void* pdy = pad.input(dy, T, O, false);
+    const void* pdy = pad.input(dy, T, O, false, plan.terms);
     void* pdx = pad.output(dx, T, H, false);
     void* pdg = pad.output(dW_gate, F, H, true);
     void* pdu = pad.output(dW_up, F, H, true);
@@ -1754,6 +1771,12 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
                             saved, pdx, pdg, pdu, pdd, ws, sms, s));
     RKL_CUDA(launch_ffn_pad(pad.out, s));
     return RKL_OK;
+  }
+  if (plan.tc && plan.terms > 1) {
+    Padding twice(ws + plan.off_pad);
+    x = twice.input(x, T, H, false, 2);
+    dy = twice.input(dy, T, O, false, 2);
+    RKL_CUDA(launch_ffn_pad(twice.in, s));
   }
   if (plan.tc)
     return ffn_backward_tc(plan, x, W_gate, W_up, W_down, activation, T, H, F, O, dy, saved, dx, dW_gate, dW_up, dW_down,

@@ -12,7 +12,8 @@
 //          u in 128..255: the epilogue rounds a = act(g) u once and stores g
 //          and u in fp32 where a backward pass wants them
 //   DGATE  da from the accumulator, g and u from memory: a, dg and du, each
-//          rounded once as the next products' operands
+//          rounded once as the next products' operands (DGATE_TERMS, for few
+//          elements: in two bf16 terms, the second as T rows more)
 //   GEMM   a list of up to four products in one launch (the backward pass runs
 //          dx, dWg, dWu and dWd together, so that one's tail is filled by
 //          another's tiles), bf16 results, or fp32 parts of a split K
@@ -24,7 +25,8 @@
 // The weights are the M operand (128 rows a tile), the rows of x the N operand;
 // every CTA streams an equal share of all (tile, K) steps, whatever tile
 // borders lie in it, and leaves fp32 parts that a small kernel joins in a fixed
-// order (with the activation between the two halves of the block).
+// order (with the activation between the two halves of the block).  For few
+// elements a is two bf16 terms, 2 T rows of the second half.
 //
 // What bounds them, with T = 8192, H = O = 2048, F = 6144:
 //   UP    0.30 ms (1.39 PFLOP/s; the tensor pipe needs 512 SM cycles for a 256 x
@@ -100,6 +102,13 @@ __device__ __forceinline__ Item item_of(const FfnPairArgs& a, int i) {
   t.lo = static_cast<int>(static_cast<long long>(steps) * t.part / p.parts);
   t.hi = static_cast<int>(static_cast<long long>(steps) * (t.part + 1) / p.parts);
   return t;
+}
+
+// What rounding to the packed pair left of two values, rounded too; 0 where the
+// rounded value is not finite, which the first term carries alone.
+__device__ __forceinline__ uint32_t rest_bf16x2(float v0, float v1, uint32_t rounded) {
+  const float h0 = __uint_as_float(rounded << 16), h1 = __uint_as_float(rounded & 0xffff0000u);
+  return pack_bf16x2(isfinite(h0) ? v0 - h0 : 0.f, isfinite(h1) ? v1 - h1 : 0.f);
 }
 
 // 32 bf16 of each of 32 rows: 16 packed words of a lane's row into one half of
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
                                act_only<ACT, true>(g[2 * e + 1]) * u[2 * e + 1]);
           store_bf16_box(buf, flip, lane, w, &p.c, x, row0, in);
         }
-      } else if (EPI == FFN_DGATE) {
+      } else if (EPI == FFN_DGATE || EPI == FFN_DGATE_TERMS) {
         const long long plane = ffn_saved_plane(p.M, p.N);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -432,20 +441,31 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           tmem_ld_32x32(tb + col, da);
           tmem_wait_ld();
           if (c == 3) release();
-          uint32_t wa[16], wg[16], wu[16];
+          uint32_t wa[16], wg[16], wu[16], ra[16], rg[16], ru[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float s0, s1;
             const float h0 = act_with_slope<ACT, true>(g[2 * e], &s0);
             const float h1 = act_with_slope<ACT, true>(g[2 * e + 1], &s1);
             const float d0 = da[2 * e], d1 = da[2 * e + 1], u0 = u[2 * e], u1 = u[2 * e + 1];
-            wa[e] = pack_bf16x2(h0 * u0, h1 * u1);
-            wg[e] = pack_bf16x2(d0 * u0 * s0, d1 * u1 * s1);
-            wu[e] = pack_bf16x2(d0 * h0, d1 * h1);
+            const float a0 = h0 * u0, a1 = h1 * u1, dg0 = d0 * u0 * s0, dg1 = d1 * u1 * s1, du0 = d0 * h0, du1 = d1 * h1;
+            wa[e] = pack_bf16x2(a0, a1);
+            wg[e] = pack_bf16x2(dg0, dg1);
+            wu[e] = pack_bf16x2(du0, du1);
+            if (EPI == FFN_DGATE_TERMS) {
+              ra[e] = rest_bf16x2(a0, a1, wa[e]);
+              rg[e] = rest_bf16x2(dg0, dg1, wg[e]);
+              ru[e] = rest_bf16x2(du0, du1, wu[e]);
+            }
           }
           store_bf16_box(buf, flip, lane, wa, &p.c, x, row0, in);
           store_bf16_box(buf, flip, lane, wg, &a.c2, x, row0, in);
           store_bf16_box(buf, flip, lane, wu, &a.c3, x, row0, in);
+          if (EPI == FFN_DGATE_TERMS) {
+            store_bf16_box(buf, flip, lane, ra, &a.rest[0], x, row0, in);
+            store_bf16_box(buf, flip, lane, rg, &a.rest[1], x, row0, in);
+            store_bf16_box(buf, flip, lane, ru, &a.rest[2], x, row0, in);
+          }
         }
       } else {
 #pragma unroll 1
@@ -457,7 +477,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) ffn_pair_kernel(const __grid_
           tmem_ld_32x32(tb + col + 32, v + 32);
           tmem_wait_ld();
           if (b == 1) release();
-          if (p.parts > 1) {
+          if (p.part_rows > 0) {
             const int y = it.part * p.part_rows + row0;
             store_f32_box(buf, lane, v, &p.c, x, y, live && x < p.N);
             store_f32_box(buf, lane, v + 32, &p.c, x + 32, y, live && x + 32 < p.N);
@@ -723,8 +743,9 @@ __device__ __forceinline__ float4 sum_parts(const FfnJoinArgs& a, long long row,
 }  // namespace
 
 // out [T, N] bf16 = the parts' sum, or (GATED) act(g) u of the sums g at column
-// n and u at a.second + n.
-template <bool GATED, int ACT>
+// n and u at a.second + n.  TERMS = 2: of the sums of rows t and T + t, or
+// (GATED) in two terms, the second at a.rest.
+template <bool GATED, int ACT, int TERMS>
 __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ FfnJoinArgs a) {
   if (threadIdx.x == 0) let_next_launch_begin();
   wait_for_last_launch();
@@ -734,6 +755,13 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ F
   const long long row = i / n4;
   const int col = static_cast<int>(i - row * n4) * 4;
   float4 v = sum_parts(a, row, col);
+  if (!GATED && TERMS == 2) {
+    const float4 r = sum_parts(a, row + a.T, col);
+    v.x += r.x;
+    v.y += r.y;
+    v.z += r.z;
+    v.w += r.w;
+  }
   const long long at = row * a.N + col;
   if (GATED) {
     const float4 u = sum_parts(a, row, a.second + col);
@@ -747,7 +775,10 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(const __grid_constant__ F
     v.z = act_only<ACT, true>(v.z) * u.z;
     v.w = act_only<ACT, true>(v.w) * u.w;
   }
-  *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  const uint2 w = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  *reinterpret_cast<uint2*>(a.out + at) = w;
+  if (GATED && TERMS == 2)
+    *reinterpret_cast<uint2*>(a.rest + at) = make_uint2(rest_bf16x2(v.x, v.y, w.x), rest_bf16x2(v.z, v.w, w.y));
 }
 
 // Matrices whose rows are not whole multiples of 16 bytes, which TMA needs, are
@@ -795,6 +826,10 @@ cudaError_t ffn_tc_setup() {
   RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE, ACT_GELU>));
   RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE, ACT_GELU_TANH>));
   RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE, ACT_RELU>));
+  RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE_TERMS, ACT_SILU>));
+  RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE_TERMS, ACT_GELU>));
+  RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE_TERMS, ACT_GELU_TANH>));
+  RKL_FFN_SETUP((ffn_pair_kernel<FFN_DGATE_TERMS, ACT_RELU>));
   RKL_FFN_SETUP((ffn_pair_kernel<FFN_GEMM, 0>));
 #undef RKL_FFN_SETUP
   return allow_smem(ffn_skinny_kernel, kSkinnySmem);
@@ -826,7 +861,7 @@ static cudaError_t launch_ffn(K kernel, unsigned grid, unsigned threads, size_t 
 }
 
 cudaError_t launch_ffn_pair(int mode, int act, const FfnPairArgs& a, int sms, cudaStream_t s) {
-  LaunchScope scope(mode == FFN_UP ? K_FFN_UP_TC : mode == FFN_DGATE ? K_FFN_DGATE_TC : K_FFN_GEMM_TC, s);
+  LaunchScope scope(mode == FFN_UP ? K_FFN_UP_TC : mode == FFN_GEMM ? K_FFN_GEMM_TC : K_FFN_DGATE_TC, s);
   const int grid = (2 * a.items < sms ? 2 * a.items : sms) & ~1;  // whole CTA pairs
   if (mode == FFN_GEMM) return launch_ffn(ffn_pair_kernel<FFN_GEMM, 0>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
   if (mode == FFN_UP) switch (act) {
@@ -834,6 +869,12 @@ cudaError_t launch_ffn_pair(int mode, int act, const FfnPairArgs& a, int sms, cu
       case ACT_GELU: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_GELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
       case ACT_GELU_TANH: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_GELU_TANH>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
       default: return launch_ffn(ffn_pair_kernel<FFN_UP, ACT_RELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+    }
+  if (mode == FFN_DGATE_TERMS) switch (act) {
+      case ACT_SILU: return launch_ffn(ffn_pair_kernel<FFN_DGATE_TERMS, ACT_SILU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+      case ACT_GELU: return launch_ffn(ffn_pair_kernel<FFN_DGATE_TERMS, ACT_GELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+      case ACT_GELU_TANH: return launch_ffn(ffn_pair_kernel<FFN_DGATE_TERMS, ACT_GELU_TANH>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
+      default: return launch_ffn(ffn_pair_kernel<FFN_DGATE_TERMS, ACT_RELU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
     }
   switch (act) {
     case ACT_SILU: return launch_ffn(ffn_pair_kernel<FFN_DGATE, ACT_SILU>, grid, kPairThreads, kPairSmem, true, a.follows, s, a);
@@ -850,17 +891,22 @@ cudaError_t launch_ffn_skinny(FfnSkinnyArgs a, int grid, cudaStream_t s) {
   return launch_ffn(ffn_skinny_kernel, grid, kSkinnyThreads, kSkinnySmem, false, a.follows, s, a);
 }
 
-cudaError_t launch_ffn_join(int act, const FfnJoinArgs& a, cudaStream_t s) {
-  LaunchScope scope(K_FFN_JOIN, s);
+template <int TERMS>
+static cudaError_t join(int act, const FfnJoinArgs& a, cudaStream_t s) {
   const long long blocks = (static_cast<long long>(a.T) * (a.N / 4) + 255) / 256;
   const unsigned grid = static_cast<unsigned>(blocks);
   switch (act) {
-    case -1: return launch_ffn(ffn_join_kernel<false, 0>, grid, 256, 0, false, true, s, a);
-    case ACT_SILU: return launch_ffn(ffn_join_kernel<true, ACT_SILU>, grid, 256, 0, false, true, s, a);
-    case ACT_GELU: return launch_ffn(ffn_join_kernel<true, ACT_GELU>, grid, 256, 0, false, true, s, a);
-    case ACT_GELU_TANH: return launch_ffn(ffn_join_kernel<true, ACT_GELU_TANH>, grid, 256, 0, false, true, s, a);
-    default: return launch_ffn(ffn_join_kernel<true, ACT_RELU>, grid, 256, 0, false, true, s, a);
+    case -1: return launch_ffn(ffn_join_kernel<false, 0, TERMS>, grid, 256, 0, false, true, s, a);
+    case ACT_SILU: return launch_ffn(ffn_join_kernel<true, ACT_SILU, TERMS>, grid, 256, 0, false, true, s, a);
+    case ACT_GELU: return launch_ffn(ffn_join_kernel<true, ACT_GELU, TERMS>, grid, 256, 0, false, true, s, a);
+    case ACT_GELU_TANH: return launch_ffn(ffn_join_kernel<true, ACT_GELU_TANH, TERMS>, grid, 256, 0, false, true, s, a);
+    default: return launch_ffn(ffn_join_kernel<true, ACT_RELU, TERMS>, grid, 256, 0, false, true, s, a);
   }
+}
+
+cudaError_t launch_ffn_join(int act, const FfnJoinArgs& a, cudaStream_t s) {
+  LaunchScope scope(K_FFN_JOIN, s);
+  return a.terms > 1 ? join<2>(act, a, s) : join<1>(act, a, s);
 }
 
 cudaError_t read_and_clear_ffn_error(int* code) {

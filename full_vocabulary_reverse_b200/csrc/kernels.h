@@ -325,7 +325,7 @@ cudaError_t launch_norm_partial(const NormArgs& a, int grid, cudaStream_t s);
 cudaError_t launch_norm_final(const double* partial, int n, float* norm, cudaStream_t s);
 
 // ---------------------------------------------------------------- gated feed-forward block
-enum : int { FFN_UP = 0, FFN_DGATE = 1, FFN_GEMM = 2 };  // what a product's results go through
+enum : int { FFN_UP = 0, FFN_DGATE = 1, FFN_GEMM = 2, FFN_DGATE_TERMS = 3 };  // what a product's results go through
 
 // g and u between the forward and the backward pass: fp32, in blocks of 32
 // rows x 32 columns (row blocks outermost), a block as 8 groups of 4 columns x
@@ -360,19 +360,31 @@ cudaError_t launch_ffn_simt(int mode, FfnSimtArgs a, int sms, cudaStream_t s);
 
 // tcgen05 path (ffn_tc_kernels.cu).
 constexpr int kFfnSkinnyRows = 128;  // rows up to which the weights are the M operand
+// Where few numbers make up the result, a, dg and du are held in two bf16 terms,
+// the second under the first as so many rows more.  Many operands' roundings
+// average: they leave a result's error (2-norm) at 1.4 times that of its own
+// rounding.  Of few, heavy-tailed ones, one large a decides: 1.6 times at T = 2,
+// F = 112; with two terms 1.0.  Up to 4096 elements of a, or 1024 of y or dx, the
+// passes are bound by their launches and two terms add 1 us to a forward pass
+// (11.7 -> 12.9) and 11 to a backward pass (22.7 -> 33.8); everywhere up to 64 rows
+// they would cost 10 percent of 1 row at H = 2048, F = 6144 and 28 of 64 rows at
+// H = 1160, F = 2712.
+constexpr int kFfnTermRows = 64;  // at most: two terms of them are one K step
+constexpr long long kFfnTermElements = 4096, kFfnTermResults = 1024;
 struct FfnPairProduct {
   CUtensorMap a[2], b[2];  // bf16, box {64, 128} K-major or {64, 64} MN-major; FFN_UP: b = Wg, Wu
-  CUtensorMap c;           // bf16 result, box {32, 32}, 64-byte swizzle; parts > 1: fp32 [parts * part_rows, N], box {32, 32}
+  CUtensorMap c;           // bf16 result, box {32, 32}, 64-byte swizzle; part_rows > 0: fp32 [parts * part_rows, N], box {32, 32}
   int M, N;
   int mt, nt;              // tiles
   int steps, segments;     // 128-deep steps of a segment of K; segments of K (1 or 2)
   int a_mn, b_mn;          // operand lies MN-major
-  int parts, part_rows;    // parts of K; rows of a part (a multiple of 32)
+  int parts, part_rows;    // parts of K; rows of an fp32 part (a multiple of 32), 0: bf16 results
   int first;               // first work item of the launch's list
 };
 struct FfnPairArgs {
   FfnPairProduct p[kFfnProducts];
   CUtensorMap c2, c3;      // FFN_DGATE: dg and du, as c
+  CUtensorMap rest[3];     // FFN_DGATE_TERMS: second terms of a, dg and du
   float* saved;            // g and u (FFN_UP: nullable)
   int* counter;            // claims work items (nullable: dealt out)
   int* zero_counter;       // set to 0 for the next launch (nullable)
@@ -391,10 +403,12 @@ struct FfnSkinnyArgs {
 struct FfnJoinArgs {
   const float* part;
   uint16_t* out;           // [T, N] bf16
+  uint16_t* rest;          // gated, two terms: the second ones
   float* saved;            // gated: g and u (nullable)
   long long pitch, slab;   // elements between rows, between parts
   long long per;           // > 0: parts as ffn_skinny_kernel numbers them; 0: `parts` everywhere
   int T, N, second, steps, parts;
+  int terms;               // 2: of a; a plain sum then adds row T + t to row t
 };
 // Copies bf16 matrices between layouts: dst (dst_rows x dst_cols, its pitch)
 // takes src (rows x cols at pitch src_pitch), zeros elsewhere.
@@ -404,7 +418,7 @@ struct FfnPadItem {
   int rows, cols, src_pitch, dst_rows, dst_cols;
   long long first;         // elements of the items before this one
 };
-constexpr int kFfnPadItems = 5;
+constexpr int kFfnPadItems = 7;
 struct FfnPadArgs {
   FfnPadItem item[kFfnPadItems];
   int n;

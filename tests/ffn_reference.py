@@ -46,15 +46,17 @@ def dot(x, w, ex, ew):
     return e
 
 
-def block(x, wg, wu, wd, kind, dy=None):
-    """[(value, bound)] of y, and with dy of dx, dWg, dWu, dWd."""
+def block(x, wg, wu, wd, kind, dy=None, operand=None):
+    """[(value, bound)] of y, and with dy of dx, dWg, dWu, dWd.  operand: what a, dg and du may be rounded by, relative
+    (None: half a step of the type)."""
     b = HALF_STEP[x.dtype]
+    o = b if operand is None else operand
     x, wg, wu, wd = (t.double() for t in (x, wg, wu, wd))
     g, u = x @ wg.t(), x @ wu.t()
     eg, eu = dot(x.abs(), wg.abs().t(), None, None), dot(x.abs(), wu.abs().t(), None, None)
     h, s = act(kind, g)
     a = h * u
-    ea = 1.13 * eg * (u.abs() + eu) + h.abs() * eu + (2.0 ** -19 + b) * a.abs()
+    ea = 1.13 * eg * (u.abs() + eu) + h.abs() * eu + (2.0 ** -19 + o) * a.abs()
     y = a @ wd.t()
     out = [(y, dot(a.abs(), wd.abs().t(), ea, None) + b * y.abs())]
     if dy is None:
@@ -63,11 +65,11 @@ def block(x, wg, wu, wd, kind, dy=None):
     da = dy @ wd
     eda = dot(dy.abs(), wd.abs(), None, None)
     du, dg = da * h, da * u * s
-    edu = h.abs() * eda + (da.abs() + eda) * 1.13 * eg + (2.0 ** -19 + b) * du.abs()
+    edu = h.abs() * eda + (da.abs() + eda) * 1.13 * eg + (2.0 ** -19 + o) * du.abs()
     es = 1.2 * eg + 2.0 ** -19 * (1 + g.abs())
     if kind == RELU:
         es = (g.abs() <= eg).double()
-    edg = (u * s).abs() * eda + ((da.abs() + eda) * (s.abs() * eu + (u.abs() + eu) * es)) + (2.0 ** -22 + b) * dg.abs()
+    edg = (u * s).abs() * eda + ((da.abs() + eda) * (s.abs() * eu + (u.abs() + eu) * es)) + (2.0 ** -22 + o) * dg.abs()
     # an output is off by its operands' bounds, its own sum's and its rounding
     dx = dg @ wg + du @ wu
     out.append((dx, dot(dg.abs(), wg.abs(), edg, None) + dot(du.abs(), wu.abs(), edu, None)

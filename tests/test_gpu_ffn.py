@@ -51,6 +51,30 @@ def test_activations(T, kind, dtype):
     both(T, 128, 200, 136, dtype, kind, seed=kind, scale=3.0)
 
 
+@pytest.mark.parametrize("kind", ACTS)
+@pytest.mark.parametrize("T,H,F,O", [(1, 64, 64, 64), (1, 1032, 2056, 520), (2, 856, 112, 256), (2, 857, 113, 255), (5, 64, 72, 2056),
+                                     (9, 136, 1000, 72), (31, 64, 128, 72), (33, 200, 77, 65), (63, 264, 64, 136), (64, 72, 64, 264)])
+def test_few_elements_round_the_result_alone(T, H, F, O, kind):
+    # a, dg and du in two terms: the rest of the first (half a step, 2^-8) is rounded by 2^-8 of itself
+    ins, dy = inputs(T, H, F, O, torch.bfloat16, T + F)
+    y, saved = ffn_forward(*ins, kind, save=True)
+    grads = ffn_backward(*ins, dy, saved, kind)
+    assert rb.device_error() == 0
+    for k, (t, (value, bound)) in enumerate(zip([y, *grads], R.block(*ins, kind, dy, operand=2.0 ** -16))):
+        off = (t.double() - value).abs()
+        assert torch.all(off <= bound), (k, float((off / bound.clamp(min=1e-300)).max()))
+
+
+def test_few_elements_that_overflow():
+    # an a beyond the type's range is infinite in its first term, with no rest beside it
+    x = torch.full((3, 8), 2.0 ** 60, dtype=torch.bfloat16, device="cuda")
+    x[1] = 1.0
+    w = torch.ones(16, 8, dtype=torch.bfloat16, device="cuda") * 8.0
+    y = ffn_forward(x, w, w, torch.ones(8, 16, dtype=torch.bfloat16, device="cuda"))[0]
+    assert torch.isinf(y[0]).all() and torch.isinf(y[2]).all()
+    assert torch.equal(y[1].float(), torch.full((8,), 65536.0, device="cuda"))  # 16 x 64 x 64
+
+
 @pytest.mark.parametrize("T", [1, 4, 16, 200])
 def test_long_and_wide(T):
     both(T, 4096, 5632, 2048, torch.bfloat16, ACT_SILU, seed=T)
