@@ -161,6 +161,11 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// Element i of a tensor of n.
+__device__ __forceinline__ void prefetch_element(const void* base, bool bf16, long long i, long long n) {
+  if (RKL_BOUNDS(i < n)) prefetch_l2(static_cast<const char*>(base) + i * (bf16 ? 2 : 4));
+}
+
 // Two fp32 values in one register pair, one instruction for both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -385,17 +390,17 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
     uint2* cv = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + s);
     const uint2 om = __ldcs(cm), ov = __ldcs(cv);
     // The next block's lines start on their way to L2: with 24 warps an SM the
-    // wait for memory showed otherwise.
-    const int ahead = gridDim.x * kWarps;
-    if (b + ahead < t_end) {
-      const long long far_on = static_cast<long long>(ahead) * kOptBlock;
+    // wait for memory showed otherwise.  (A lane whose elements lie behind the
+    // tensor's end, in its last block, has nothing to fetch.)
+    const long long far_on = static_cast<long long>(gridDim.x) * kWarps * kOptBlock;
+    if (i + far_on < x.n) {
       prefetch_l2(cm + far_on / 8);
       prefetch_l2(cv + far_on / 8);
-      prefetch_l2(static_cast<const char*>(x.grad) + (i + far_on) * (x.flags & OPT_GRAD_BF16 ? 2 : 4));
+      prefetch_element(x.grad, x.flags & OPT_GRAD_BF16, i + far_on, x.n);
       if (a.master != nullptr)
         prefetch_l2(a.master + s + far_on);
       else
-        prefetch_l2(static_cast<const char*>(x.param) + (i + far_on) * (x.flags & OPT_PARAM_BF16 ? 2 : 4));
+        prefetch_element(x.param, x.flags & OPT_PARAM_BF16, i + far_on, x.n);
     }
     const float ms = a.m_scale[q], vs = a.v_scale[q];
     uint64_t m[4], v[4], term[4];  // neighbouring elements in pairs
