@@ -224,6 +224,19 @@ __device__ __forceinline__ double e4m3_to_f64(uint32_t code) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(code & 0xffu)));
   return static_cast<double>(__half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xffffu))));
 }
+// Which of a lane's 8 second moments are above 0 by what they are made of, the
+// gradients or (where those count) the old codes: 1 in the byte of each.
+__device__ __noinline__ uint2 above_zero(const void* grad, uint32_t flags, long long i, long long n, uint2 old, bool kept) {
+  float g[8];
+  load8(grad, flags & OPT_GRAD_BF16, flags & OPT_WIDE_GRAD, i, n, g);
+  uint32_t one[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool was = kept && (((e < 4 ? old.x : old.y) >> (8 * (e & 3))) & 0x7f) != 0;
+    if (g[e] != 0.f || was) one[e / 4] |= 1u << (8 * (e & 3));
+  }
+  return make_uint2(one[0], one[1]);
+}
 struct Exact {
   double beta1, beta2, clip, m_scale, v_scale;
 };
@@ -353,9 +366,10 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
 
 // 8-bit moments: 10 bytes an element with bf16 parameters and gradients.  The
 // arithmetic (about 70 instructions an element, most of them the codes' and the
-// random numbers') and not memory sets the time: 349 M elements take 1.0 to 1.35
-// ms, by how many blocks look again in 64 bits (2 in 100 on changing gradients,
-// about 15 where the gradient stays the same and moments stop next to borders).
+// random numbers') and the waits of 24 warps an SM set the time, not memory: 349 M
+// elements take 1.0 to 1.35 ms, by how many blocks look again in 64 bits (2 in 100
+// on changing gradients, about 15 where the gradient stays the same and moments
+// stop next to borders).
 // Paired fp32 instructions took 10 % of the instructions away; 24 warps an SM
 // with the next block's lines on their way to L2 ran faster than 16 or 32.
 //
@@ -367,7 +381,13 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
 //      block's largest by 5 u of its own t; r by 2 u more: below
 //      t 448 / largest u (7 + 5 W), W the block's largest t over the largest.
 //   v: all terms are positive, 7 u; the largest as much, r 2 u more: 16 u of r,
-//      and a code's step is r / 16 at least.
+//      and a code's step is r / 16 at least.  Below fp32's normal numbers a term
+//      is off by up to 2^-149, that is 2^-40 of r in a block that has a scale (16
+//      u of the smallest code's step are 2^-29); whether v is above 0 is then
+//      asked of what it is made of: where a code came out as 0, which blocks of
+//      moments near each other do not have (blocks that hold moments of 0 beside
+//      others take 15 % longer for it; a look at every gradient would take 3 %
+//      everywhere).
 __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_constant__ AdamwArgs a) {
   __shared__ StepConsts k;
   begin_step(a, &k);
@@ -449,7 +469,6 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
     const float mi = m_some ? __fdiv_rn(kE4m3Max, mm) : 0.f, vi = v_some ? __fdiv_rn(kE4m3Max, vm) : 0.f;
     const bool far = vm > kLargeV;  // vi 2^-120 leaves fp32's normal range: all of v in 64 bits
     const float vi120 = vi * 7.52316384526264e-37f;
-    const uint32_t least = v_some ? 0x01000000u : 0u;
     // First moment to the nearest code: b1 leaves each step a tenth of a new
     // value, above the half step of the code.  Second moment stochastically:
     // with b2 = 0.999 a step moves it by less than half a code's step, and to
@@ -486,14 +505,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
       m[e] = mul2(m[e], pair(mi, mi));
       const float2 d = in_reach(m[e], term[e]);
       reach = max3_nan(reach, d.x, d.y);
-      const float2 vf = both(v[e]), r120 = both(mul2(v[e], pair(vi120, vi120)));
-      const uint32_t y0 = raised(r120.x, 2 * e), y1 = raised(r120.y, 2 * e + 1);
-      nearest_v = min(min(nearest_v, v_window(y0)), v_window(y1));
-      // not to 0 from above it: a second moment of 0 beside a first moment that
-      // is not would blow the next update up.  (The largest value's carry out of
-      // the last code is next to a border.)
-      y[2 * e] = max(y0, min(__float_as_uint(vf.x), 1u) * least);
-      y[2 * e + 1] = max(y1, min(__float_as_uint(vf.y), 1u) * least);
+      const float2 r120 = both(mul2(v[e], pair(vi120, vi120)));
+      y[2 * e] = raised(r120.x, 2 * e);
+      y[2 * e + 1] = raised(r120.y, 2 * e + 1);
+      // (the largest value's carry out of the last code is next to a border)
+      nearest_v = min(min(nearest_v, v_window(y[2 * e])), v_window(y[2 * e + 1]));
     }
     float mq[8];
 #pragma unroll
@@ -502,55 +518,70 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
       mq[2 * e] = f.x;
       mq[2 * e + 1] = f.y;
     }
-    const bool near_m = __any_sync(kAll, !(reach < 0.f)) && m_some;
-    const bool near_v = far || __any_sync(kAll, nearest_v < (kVNear << 9));
-    if (near_m || near_v) {
-      const Exact z{a.beta1_64, a.beta2_64, k.clip64, ms, vs};
-      float g[8];
-      load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i, x.n, g);
-      if (near_m) {
-        double most = 0;  // among those that may be the largest
-        const float least_r = kE4m3Max * fmaf(w, -16.f * kUlp, 1.f);
+    uint2 code_v = make_uint2(top_bytes(y[0], y[1], y[2], y[3]), top_bytes(y[4], y[5], y[6], y[7]));
+    // Codes of 0: bytes are at most 0x7e, adding 0x7f reaches a byte's top bit from 1 on.
+    const bool zero = ((code_v.x + 0x7f7f7f7fu) & (code_v.y + 0x7f7f7f7fu) & 0x80808080u) != 0x80808080u && v_some;
+    // (one vote where, as mostly, there is nothing to look at again)
+    if (far || __any_sync(kAll, (!(reach < 0.f) && m_some) || nearest_v < (kVNear << 9) || zero)) {
+      const bool near_m = __any_sync(kAll, !(reach < 0.f)) && m_some;
+      const bool near_v = far || __any_sync(kAll, nearest_v < (kVNear << 9));
+      if (near_m || near_v) {
+        const Exact z{a.beta1_64, a.beta2_64, k.clip64, ms, vs};
+        float g[8];
+        load8(x.grad, x.flags & OPT_GRAD_BF16, x.flags & OPT_WIDE_GRAD, i, x.n, g);
+        if (near_m) {
+          double most = 0;  // among those that may be the largest
+          const float least_r = kE4m3Max * fmaf(w, -16.f * kUlp, 1.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!(fabsf(mq[e]) < least_r)) most = fmax(most, fabs(exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e])));
-        most = warp_max(most);
-        const double inv = 448.0 / most;
+          for (int e = 0; e < 8; ++e)
+            if (!(fabsf(mq[e]) < least_r)) most = fmax(most, fabs(exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e])));
+          most = warp_max(most);
+          const double inv = 448.0 / most;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 d = in_reach(m[e / 2], term[e / 2]);
-          if (!((e & 1 ? d.y : d.x) < 0.f)) {
-            const double r = exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e]) * inv;
-            const double gap = e4m3_step(fabs(r));
-            mq[e] = static_cast<float>(rint(r * inverse_of(gap)) * gap);
+          for (int e = 0; e < 8; ++e) {
+            const float2 d = in_reach(m[e / 2], term[e / 2]);
+            if (!((e & 1 ? d.y : d.x) < 0.f)) {
+              const double r = exact_m(z, (e < 4 ? om.x : om.y) >> (8 * (e & 3)), g[e]) * inv;
+              const double gap = e4m3_step(fabs(r));
+              mq[e] = static_cast<float>(rint(r * inverse_of(gap)) * gap);
+            }
+          }
+        }
+        if (near_v) {
+          double most = 0;
+          const float least_v = far ? 0.f : vm * (1.f - 32.f * kUlp);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 vf = both(v[e / 2]);
+            if (!((e & 1 ? vf.y : vf.x) < least_v)) most = fmax(most, exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]));
+          }
+          most = warp_max(most);
+          const double inv = v_some ? 448.0 / most : 0.0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 r120 = both(mul2(v[e / 2], pair(vi120, vi120)));
+            if (far || v_window(raised(e & 1 ? r120.y : r120.x, e)) < (kVNear << 9)) {
+              const double r = exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]) * inv;
+              const double gap = e4m3_step(r);
+              const double up =
+                  floor(r * inverse_of(gap) + (mix32(place ^ static_cast<uint32_t>(e)) >> 12) * 9.5367431640625e-7) * gap;
+              const uint32_t code = __float_as_uint(static_cast<float>(up) * 7.52316384526264e-37f) >> 20;
+              y[e] = min(max(code, r > 0 ? 1u : 0u), 126u) << 24;
+            }
           }
         }
       }
-      if (near_v) {
-        double most = 0;
-        const float least_v = far ? 0.f : vm * (1.f - 32.f * kUlp);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 vf = both(v[e / 2]);
-          if (!((e & 1 ? vf.y : vf.x) < least_v)) most = fmax(most, exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]));
-        }
-        most = warp_max(most);
-        const double inv = v_some ? 448.0 / most : 0.0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 r120 = both(mul2(v[e / 2], pair(vi120, vi120)));
-          if (far || v_window(raised(e & 1 ? r120.y : r120.x, e)) < (kVNear << 9)) {
-            const double r = exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]) * inv;
-            const double gap = e4m3_step(r);
-            const double up =
-                floor(r * inverse_of(gap) + (mix32(place ^ static_cast<uint32_t>(e)) >> 12) * 9.5367431640625e-7) * gap;
-            const uint32_t code = __float_as_uint(static_cast<float>(up) * 7.52316384526264e-37f) >> 20;
-            y[e] = min(max(code, r > 0 ? 1u : 0u), 126u) << 24;
-          }
-        }
+      if (near_v) code_v = make_uint2(top_bytes(y[0], y[1], y[2], y[3]), top_bytes(y[4], y[5], y[6], y[7]));
+      // Codes of 0, rare but where a moment is 0: not from above it, in fp32 or
+      // not.  A second moment of 0 beside a first moment that is not would blow
+      // the next update up.
+      if (__any_sync(kAll, zero)) {
+        const uint2 one = above_zero(x.grad, x.flags, i, x.n, ov, a.beta2_64 > 0 && vs > 0.f);
+        code_v.x |= one.x & ~((code_v.x + 0x7f7f7f7fu) >> 7);
+        code_v.y |= one.y & ~((code_v.y + 0x7f7f7f7fu) >> 7);
       }
     }
-    *cv = make_uint2(top_bytes(y[0], y[1], y[2], y[3]), top_bytes(y[4], y[5], y[6], y[7]));
+    *cv = code_v;
     *cm = pack_e4m3x8(mq);
     if (lane == 0) {
       a.m_scale[q] = m_some ? mm * (1.f / kE4m3Max) : 0.f;

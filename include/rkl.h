@@ -490,7 +490,8 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
  *     a value is code x scale of its block of 256, scale = largest magnitude /
  *     448.  A block no larger than 2^-100 is held as zeros.  exp_avg is rounded
  *     to the nearest code (ties to even).  exp_avg_sq is rounded stochastically:
- *     up when rest + r / 2^20 >= 1, and never from a positive value to 0, with
+ *     up when rest + r / 2^20 >= 1, and never from a positive value to 0 (one
+ *     whose gradient or old value is not 0, also where fp32 cannot hold it), with
  *     the 20-bit number r = mix(e ^ mix(key + (e >> 32))) >> 12 of element e of
  *     the state, key = mix(t x 0x9E3779B1 + seed), all in 32 bits and mix the
  *     final mix of MurmurHash3.  Equal calls give equal bits.

@@ -1,0 +1,82 @@
+"""AdamW at the ends of its range: second moments below and above fp32's,
+scales, no eps.  Codes and scales against the 64-bit formulas of
+optim_reference.py."""
+
+import math
+
+import pytest
+import torch
+
+from full_vocabulary_reverse_b200 import AdamW
+from full_vocabulary_reverse_b200 import binding as rb
+from tests import optim_reference as R
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+LR, BETAS, EPS = 3e-3, (0.9, 0.999), 1e-8
+
+
+def state(opt):
+    """(m, v) of the 8-bit state's one tensor, code x scale in float64 on the CPU."""
+    n = opt.params[0].numel()
+    return tuple((x.double().view(-1, 256) * s.double()[:, None]).view(-1)[:n].cpu()
+                 for x, s in ((opt.exp_avg, opt.exp_avg_scale), (opt.exp_avg_sq, opt.exp_avg_sq_scale)))
+
+
+def after(opt, g, t, betas=BETAS, clip=1.0):
+    """(m, v) that a step makes of the state, in float64."""
+    m, v = state(opt)
+    _, m, v = R.adamw(torch.zeros_like(m), m, v, g.double().cpu(), t, LR, betas, EPS, 0.0, clip)
+    return m, v
+
+
+def same(codes, ref):
+    # (2^-40 of a step: the order of the reference's own 64-bit operations)
+    value, _, edge, _, _ = ref
+    return not ((codes.double().cpu() != value) & (edge > 2.0 ** -40)).any()
+
+
+def mixed(n, small, seed):
+    """Gradients near 1e-3, of `small` size and 0, side by side in every block."""
+    gen = torch.Generator().manual_seed(seed)
+    g = torch.randn(n, generator=gen) * 1e-3
+    g[1::3] = torch.randn(g[1::3].shape, generator=gen).abs() * small + small
+    g[2::5] = 0.0
+    return g.cuda()
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("small,max_norm", [(1e-22, None), (1e-26, None), (1e-16, 4e-8), (1e-30, 1e-4)])
+def test_second_moments_below_fp32_are_not_zero(small, max_norm, grad):
+    """A gradient whose square fp32 cannot hold still makes a second moment above 0, whose code is never 0."""
+    n = 4096 + 77
+    g = mixed(n, small, 3).to(grad)
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=BETAS, eps=EPS, weight_decay=0.0, state_bits=8, seed=6)
+    for t in (1, 2):
+        zero = (state(opt)[1] == 0) & (g.cpu() == 0)
+        norm = opt.step([g], max_norm=max_norm) if t == 1 else opt.step([g])
+        if t == 1:
+            fresh = AdamW([torch.zeros(n, device="cuda")], state_bits=8)
+            m, v = after(fresh, g, t, clip=1.0 if norm is None else min(1.0, max_norm / float(norm)))
+        else:
+            m, v = after(kept, g, t)
+        assert same(opt.exp_avg, R.codes(m)), t
+        assert same(opt.exp_avg_sq, R.codes(v, R.random20(torch.arange(n), t, 6))), t
+        code = opt.exp_avg_sq[:n].view(torch.uint8).cpu()
+        assert (code[zero] == 0).all() and (code[~zero] > 0).all()
+        kept = AdamW([torch.zeros(n, device="cuda")], state_bits=8)
+        kept.load_state_dict(opt.state_dict())
+    assert rb.device_error() == 0 and opt.params[0].isfinite().all()
+
+
+def test_second_moment_that_beta2_takes_below_fp32_is_not_zero():
+    """The old moment times a beta2 below fp32's normal numbers, beside new gradients and zeros."""
+    n, betas = 1024, (0.9, 1e-42)
+    g = mixed(n, 1e-3, 4)
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=betas, weight_decay=0.0, state_bits=8, seed=1)
+    opt.step([g])
+    turned = torch.where(g == 0, torch.full_like(g, 1e-3), torch.zeros_like(g))
+    m, v = after(opt, turned, 2, betas)
+    opt.step([turned])
+    assert (v > 0).all() and (opt.exp_avg_sq.view(torch.uint8) > 0).all()
+    assert same(opt.exp_avg_sq, R.codes(v, R.random20(torch.arange(n), 2, 1)))
