@@ -128,6 +128,8 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kTinyBlock = 7.888609e-31f;  // 2^-100: a block no larger than this is held as zeros (its scale's
                                              // reciprocal would leave the range of fp32)
 constexpr float kLargeV = 16384.f;
+constexpr double kLargest = 3.4028234663852886e38;  // of fp32
+constexpr double kInfinity = HUGE_VAL;
 constexpr float kUlp = 5.9604645e-8f;        // 2^-24
 constexpr uint32_t kVNear = 17u << 4;        // fp32's error of v's place between two codes, in 2^-24 of the way
 
@@ -556,6 +558,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
             if (!((e & 1 ? vf.y : vf.x) < least_v)) most = fmax(most, exact_v(z, (e < 4 ? ov.x : ov.y) >> (8 * (e & 3)), g[e]));
           }
           most = warp_max(most);
+          if (far) {  // in 64 bits too: vm may be infinite where the scale is not
+            if (most < kInfinity) most = fmin(most, 448.0 * kLargest);
+            if (lane == 0) a.v_scale[q] = static_cast<float>(most / 448.0);
+          }
           const double inv = v_some ? 448.0 / most : 0.0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
     *cm = pack_e4m3x8(mq);
     if (lane == 0) {
       a.m_scale[q] = m_some ? mm * (1.f / kE4m3Max) : 0.f;
-      a.v_scale[q] = v_some ? vm * (1.f / kE4m3Max) : 0.f;
+      if (!far) a.v_scale[q] = v_some ? vm * (1.f / kE4m3Max) : 0.f;
     }
   }
 }

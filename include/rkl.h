@@ -488,13 +488,18 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
  *   state_bits = 32: exp_avg and exp_avg_sq are fp32 [total]; no scales.
  *   state_bits = 8:  they are e4m3 codes [total] and fp32 scales [total / 256];
  *     a value is code x scale of its block of 256, scale = largest magnitude /
- *     448.  A block no larger than 2^-100 is held as zeros.  exp_avg is rounded
- *     to the nearest code (ties to even).  exp_avg_sq is rounded stochastically:
- *     up when rest + r / 2^20 >= 1, and never from a positive value to 0 (one
- *     whose gradient or old value is not 0, also where fp32 cannot hold it), with
- *     the 20-bit number r = mix(e ^ mix(key + (e >> 32))) >> 12 of element e of
- *     the state, key = mix(t x 0x9E3779B1 + seed), all in 32 bits and mix the
- *     final mix of MurmurHash3.  Equal calls give equal bits.
+ *     448 (and no scale above fp32's largest number: a larger second moment
+ *     counts as 448 times that).  A block no larger than 2^-100 is held as zeros.
+ *     exp_avg is rounded to the nearest code (ties to even).  exp_avg_sq is rounded
+ *     stochastically: up when rest + r / 2^20 >= 1, and never from a positive
+ *     value to 0 (one whose gradient or old value is not 0, also where fp32 cannot
+ *     hold it), with the 20-bit number r = mix(e ^ mix(key + (e >> 32))) >> 12 of
+ *     element e of the state, key = mix(t x 0x9E3779B1 + seed), all in 32 bits and
+ *     mix the final mix of MurmurHash3.  Equal calls give equal bits.
+ * A finite gradient whose second moment fp32 cannot hold (from 5.8e20 with beta2 =
+ * 0.999) takes no update of its own; with state_bits = 32 that moment stays
+ * infinite.  An infinite or NaN gradient of a step without norm reaches its own
+ * moments (state_bits = 8: through the scales, those of its block).
  * master (fp32 [total], nullable): the parameters themselves in the state's
  * layout; params then receive the rounded copies and are not read.
  * control: int32 [2], 8-byte aligned, {steps done, 0} between steps.  The step

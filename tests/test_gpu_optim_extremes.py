@@ -80,3 +80,33 @@ def test_second_moment_that_beta2_takes_below_fp32_is_not_zero():
     opt.step([turned])
     assert (v > 0).all() and (opt.exp_avg_sq.view(torch.uint8) > 0).all()
     assert same(opt.exp_avg_sq, R.codes(v, R.random20(torch.arange(n), 2, 1)))
+
+
+@pytest.mark.parametrize("size", [1e21, 2e23, 3e38])
+def test_second_moment_above_fp32_leaves_its_neighbours_alone(size):
+    """One gradient whose square fp32 cannot hold: the block's scale is the formula's, the largest number at most, and
+    the values beside it stay finite, zeros stay zeros."""
+    n, top = 512, torch.finfo(torch.float32).max
+    g = mixed(n, 1e-4, 9)
+    g[7] = size
+    g[300] = 0.25
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=BETAS, eps=EPS, weight_decay=0.0, state_bits=8, seed=2)
+    for t in (1, 2, 3):
+        _, v = after(opt, g, t)
+        opt.step([g])
+        scale = opt.exp_avg_sq_scale.double().cpu()
+        assert scale.isfinite().all() and opt.params[0].isfinite().all()
+        largest = float(v[:256].max())
+        assert abs(float(scale[0]) - min(largest / 448, top)) <= 2.0 ** -24 * float(scale[0])
+        if largest / 448 <= top:  # codes of the first block: the formula's
+            assert same(opt.exp_avg_sq[:256], R.codes(v[:256], R.random20(torch.arange(256), t, 2)))
+        code = opt.exp_avg_sq.view(torch.uint8).cpu()
+        assert code[7] == 126 and (code[(g == 0).cpu()] == 0).all() and (code[(g != 0).cpu()] > 0).all()
+    # the other block is as it would be without its neighbour
+    twin = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=BETAS, eps=EPS, weight_decay=0.0, state_bits=8, seed=2)
+    h = g.clone()
+    h[7] = 0.0
+    for _ in range(3):
+        twin.step([h])
+    assert torch.equal(twin.params[0][256:], opt.params[0][256:])
+    assert torch.equal(twin.exp_avg_sq.view(torch.uint8)[256:], opt.exp_avg_sq.view(torch.uint8)[256:])
