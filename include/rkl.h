@@ -488,7 +488,7 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
  *   state_bits = 32: exp_avg and exp_avg_sq are fp32 [total]; no scales.
  *   state_bits = 8:  they are e4m3 codes [total] and fp32 scales [total / 256];
  *     a value is code x scale of its block of 256, scale = largest magnitude /
- *     448 (and no scale above fp32's largest number: a larger second moment
+ *     448, the fp32 quotient (and no scale above fp32's largest number: a larger second moment
  *     counts as 448 times that).  A block no larger than 2^-100 is held as zeros.
  *     exp_avg is rounded to the nearest code (ties to even).  exp_avg_sq is rounded
  *     stochastically: up when rest + r / 2^20 >= 1, and never from a positive

@@ -110,3 +110,15 @@ def test_second_moment_above_fp32_leaves_its_neighbours_alone(size):
         twin.step([h])
     assert torch.equal(twin.params[0][256:], opt.params[0][256:])
     assert torch.equal(twin.exp_avg_sq.view(torch.uint8)[256:], opt.exp_avg_sq.view(torch.uint8)[256:])
+
+
+def test_scales_are_the_rounded_quotient():
+    """Where fp32 holds a block's largest exactly (betas of 0: the gradient and its square), its scale is that number
+    over 448, rounded once."""
+    n = 256 * 4000
+    g = torch.randn(n, generator=torch.Generator().manual_seed(8)).bfloat16()
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=(0.0, 0.0), weight_decay=0.0, state_bits=8)
+    opt.step([g.cuda()])
+    most = g.double().abs().view(-1, 256).amax(1)
+    assert torch.equal(opt.exp_avg_scale.cpu(), (most / 448).float())
+    assert torch.equal(opt.exp_avg_sq_scale.cpu(), (most * most / 448).float())
