@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1229,7 +1230,9 @@ rkl_status rkl_adamw_step(int32_t n, void* const* params, const void* const* gra
   a.omb2 = static_cast<float>(1 - beta2);
   a.log_beta1 = static_cast<float>(log(beta1));  // -inf for 0: 1 - b^t = 1
   a.log_beta2 = static_cast<float>(log(beta2));
-  a.eps = static_cast<float>(eps);
+  // With v = 0 too, 0 / eps has to stay 0 (the elements between two tensors): no
+  // less than the smallest number whose reciprocal the kernels' approximation has.
+  a.eps = eps < FLT_MIN ? FLT_MIN : static_cast<float>(eps);
   a.beta1_64 = beta1;
   a.beta2_64 = beta2;
   a.max_norm = max_norm;

@@ -481,6 +481,9 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
  *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
  *     p = p (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
+ * An eps below fp32's smallest normal number (0 is allowed) counts as that number:
+ * an element whose moments are 0 is not updated.
+ *
  * The moments of all tensors are two flat arrays; rkl_adamw_state_size gives
  * the first element at[i] of each tensor (a multiple of 256) and the arrays'
  * length.  Elements between a tensor's end and the next tensor's start belong
@@ -488,8 +491,9 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
  *   state_bits = 32: exp_avg and exp_avg_sq are fp32 [total]; no scales.
  *   state_bits = 8:  they are e4m3 codes [total] and fp32 scales [total / 256];
  *     a value is code x scale of its block of 256, scale = largest magnitude /
- *     448, the fp32 quotient (and no scale above fp32's largest number: a larger second moment
- *     counts as 448 times that).  A block no larger than 2^-100 is held as zeros.
+ *     448, the fp32 quotient (and no scale above fp32's largest number: a larger
+ *     second moment counts as 448 times that).  A block no larger than 2^-100 is
+ *     held as zeros.
  *     exp_avg is rounded to the nearest code (ties to even).  exp_avg_sq is rounded
  *     stochastically: up when rest + r / 2^20 >= 1, and never from a positive
  *     value to 0 (one whose gradient or old value is not 0, also where fp32 cannot

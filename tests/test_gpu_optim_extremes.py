@@ -122,3 +122,21 @@ def test_scales_are_the_rounded_quotient():
     most = g.double().abs().view(-1, 256).amax(1)
     assert torch.equal(opt.exp_avg_scale.cpu(), (most / 448).float())
     assert torch.equal(opt.exp_avg_sq_scale.cpu(), (most * most / 448).float())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_no_eps_leaves_the_elements_between_tensors_zero(bits):
+    counts = [257, 3, 256]
+    gen = torch.Generator().manual_seed(1)
+    ps = [torch.randn(n, generator=gen).cuda() for n in counts]
+    gs = [torch.randn(n, generator=gen).cuda() for n in counts]
+    opt = AdamW(ps, lr=LR, betas=BETAS, eps=0.0, weight_decay=0.1, state_bits=bits, master_weights=True)
+    old = [p.double().cpu() for p in ps]
+    opt.step(gs)
+    for p, g, p0, at in zip(ps, gs, old, opt.offsets):
+        z = torch.zeros_like(p0)
+        ref, _, _ = R.adamw(p0, z, z, g.double().cpu(), 1, LR, BETAS, 0.0, 0.1)
+        assert torch.all((p.double().cpu() - ref).abs() <= 4 * U * ref.abs() + 2.0 ** -19 * LR)
+        pad = slice(at + p.numel(), at + -(-p.numel() // 256) * 256)
+        for x in (opt.master, opt.exp_avg.float(), opt.exp_avg_sq.float()):
+            assert not x[pad].any()
