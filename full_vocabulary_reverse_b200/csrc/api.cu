@@ -1232,7 +1232,11 @@ rkl_status rkl_adamw_step(int32_t n, void* const* params, const void* const* gra
   a.log_beta2 = static_cast<float>(log(beta2));
   // With v = 0 too, 0 / eps has to stay 0 (the elements between two tensors): no
   // less than the smallest number whose reciprocal the kernels' approximation has.
-  a.eps = eps < FLT_MIN ? FLT_MIN : static_cast<float>(eps);
+  // 8-bit states: no less than what v below fp32's normal numbers, which that kernel
+  // takes as 0, comes from (gradients of 3.4e-18 with beta2 = 0.999; blocks of v up
+  // to 2^-100, gradients of 3e-14, have no digits there at all).
+  const float least_eps = state_bits == 8 ? 3.469446951953614e-18f : FLT_MIN;
+  a.eps = eps < least_eps ? least_eps : static_cast<float>(eps);
   a.beta1_64 = beta1;
   a.beta2_64 = beta2;
   a.max_norm = max_norm;

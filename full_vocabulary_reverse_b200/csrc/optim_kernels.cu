@@ -311,11 +311,11 @@ __device__ __forceinline__ void begin_step(const AdamwArgs& a, StepConsts* c) {
 }
 
 // p from the new moments: square root and quotient by the hardware's
-// approximations (2^-22 each).  The update is lr times smaller than p's own
+// approximations (2^-22 each; a v below the normal numbers has its root).  The update is lr times smaller than p's own
 // scale, its last bits are lost in p.
 __device__ __forceinline__ float new_param(float p, float m, float v, float keep, float step, float root, float eps) {
   float sq, inv;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(sq) : "f"(v));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(sq) : "f"(v));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(sq, root, eps)));
   return fmaf(p, keep, -(step * m) * inv);
 }
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) adamw8_kernel(const __grid_con
         term[e] = pair(t0, t1);
         v[e] = fma2(mul2(ge, pair(a.omb2, a.omb2)), ge, mul2(pair(vc[2 * e], vc[2 * e + 1]), pair(vk, vk)));
         const float2 vf = both(v[e]);
-        // (as new_param does)
+        // (as new_param does; a v below the normal numbers counts as 0, which eps is above)
         float q0, q1, r0, r1;
         asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(vf.x));
         asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(vf.y));

@@ -481,8 +481,8 @@ rkl_status rkl_ffn_backward(const void* x, const void* W_gate, const void* W_up,
  *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
  *     p = p (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
- * An eps below fp32's smallest normal number (0 is allowed) counts as that number:
- * an element whose moments are 0 is not updated.
+ * An eps below fp32's smallest normal number (0 is allowed), or with 8-bit states
+ * below 2^-58, counts as that number: an element whose moments are 0 is not updated.
  *
  * The moments of all tensors are two flat arrays; rkl_adamw_state_size gives
  * the first element at[i] of each tensor (a multiple of 256) and the arrays'

@@ -140,3 +140,33 @@ def test_no_eps_leaves_the_elements_between_tensors_zero(bits):
         pad = slice(at + p.numel(), at + -(-p.numel() // 256) * 256)
         for x in (opt.master, opt.exp_avg.float(), opt.exp_avg_sq.float()):
             assert not x[pad].any()
+
+
+@pytest.mark.parametrize("size", [1e-17, 1e-19, 3e-21])
+def test_no_eps_and_second_moments_below_the_normal_numbers(size):
+    """32-bit states without eps: a first step moves by lr whatever the gradient's size.  v = (1 - b2) g^2 is off by the
+    half steps of two operations, 2^-149 in all, beside the 12 u of a normal v; its root by half of that, relative."""
+    n = 300
+    gen = torch.Generator().manual_seed(7)
+    g = ((torch.rand(n, generator=gen) + 1) * size * (torch.randint(0, 2, (n,), generator=gen) * 2 - 1)).cuda()
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=BETAS, eps=0.0, weight_decay=0.0)
+    opt.step([g])
+    z = torch.zeros(n, dtype=torch.float64)
+    ref, _, v = R.adamw(z, z, z, g.double().cpu(), 1, LR, BETAS, 0.0, 0.0)
+    part = 2.0 ** -149 / v
+    assert (part < 0.5).all()
+    assert torch.all((opt.params[0].double().cpu() - ref).abs() <= LR * (2.0 ** -19 + part))
+
+
+def test_no_eps_and_faint_gradients_in_8_bits():
+    """Beside larger gradients, where their second moment has no digits: no update goes beyond lr."""
+    n = 2048
+    gen = torch.Generator().manual_seed(5)
+    size = 10.0 ** (torch.randint(-24, -2, (n,), generator=gen))
+    g = ((torch.rand(n, generator=gen) + 1) * size * (torch.randint(0, 2, (n,), generator=gen) * 2 - 1)).cuda()
+    opt = AdamW([torch.zeros(n, device="cuda")], lr=LR, betas=BETAS, eps=0.0, weight_decay=0.0, state_bits=8)
+    opt.step([g])
+    p = opt.params[0]
+    assert (p.abs() <= LR * (1 + 2.0 ** -18)).all() and (p * g <= 0).all()
+    large = g.abs() >= 1e-14
+    assert torch.all((p.abs() - LR)[large].abs() <= LR * 2.0 ** -11)  # eps beside 1e-14: 2^-58 / 1e-14 < 2^-11
