@@ -1426,6 +1426,7 @@ struct FfnPlan {
   size_t off_counter = 0, off_part = 0, total = 0;
   bool padded = false;                 // bf16 of odd widths: copies at off_pad (backward, two terms: x and dy)
   size_t off_pad = 0;
+  int64_t inner = 0;                   // F without its padding
 };
 
 static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_t O, bool backward) {
@@ -1436,6 +1437,7 @@ static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_
     const int64_t Hp = (H + 7) / 8 * 8, Fp = (F + 7) / 8 * 8, Op = (O + 7) / 8 * 8;
     p = ffn_plan(dtype, T, Hp, Fp, Op, backward);
     p.padded = true;
+    p.inner = F;
     p.off_pad = align256(p.total);
     const size_t x = align256(T * Hp * 2), wide = align256(Fp * Hp * 2), down = align256(Op * Fp * 2),
                  y = align256(T * Op * 2);
@@ -1443,6 +1445,7 @@ static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_
     return p;
   }
   if (p.tc && T <= kFfnTermRows && (T * F <= kFfnTermElements || T * (H < O ? H : O) <= kFfnTermResults)) p.terms = 2;
+  p.inner = F;
   p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 * p.terms : 4);
   p.off_counter = align256((backward ? 3 : 1) * p.plane);
   p.off_part = p.off_counter + 256;
@@ -1475,9 +1478,9 @@ static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_
 }
 
 // Map of a bf16 operand: `rows` x `cols` row-major, read K-major (K = columns)
-// or MN-major (K = rows).
-static rkl_status operand_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool mn) {
-  return make_map(m, p, false, cols, rows, cols * 2, kBK, mn ? kBK : 128);
+// or MN-major (K = rows).  live > 0: columns from there on read as zeros.
+static rkl_status operand_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool mn, int64_t live = 0) {
+  return make_map(m, p, false, live > 0 ? live : cols, rows, cols * 2, kBK, mn ? kBK : 128);
 }
 
 // Map of a bf16 result, stored in 32 x 32 boxes.
@@ -1486,14 +1489,16 @@ static rkl_status result_map(CUtensorMap* m, const void* p, int64_t rows, int64_
 }
 
 // One product of a launch's list: A and B row-major as they lie, `*_mn` where K
-// is their row index.
+// is their row index.  a_live > 0: columns of A (K-major) from there on are
+// padding, which may hold anything: act(g) u of an infinite row of x is infinity
+// x 0 there.
 static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bool a_mn, const void* B, const void* B2,
-                               bool b_mn, void* C, int64_t M, int64_t N, int64_t K, bool up, int parts = 1,
-                               int part_rows = 0) {
+                               bool b_mn, void* C, int64_t M, int64_t N, int64_t K, bool up, int64_t a_live = 0,
+                               int parts = 1, int part_rows = 0) {
   FfnPairProduct& p = a.p[a.n++];
-  RKL_TRY(operand_map(&p.a[0], A, a_mn ? K : M, a_mn ? M : K, a_mn));
+  RKL_TRY(operand_map(&p.a[0], A, a_mn ? K : M, a_mn ? M : K, a_mn, a_live));
   p.a[1] = p.a[0];
-  if (A2) RKL_TRY(operand_map(&p.a[1], A2, a_mn ? K : M, a_mn ? M : K, a_mn));
+  if (A2) RKL_TRY(operand_map(&p.a[1], A2, a_mn ? K : M, a_mn ? M : K, a_mn, a_live));
   RKL_TRY(operand_map(&p.b[0], B, b_mn ? K : N, b_mn ? N : K, b_mn));
   p.b[1] = p.b[0];
   if (B2) RKL_TRY(operand_map(&p.b[1], B2, b_mn ? K : N, b_mn ? N : K, b_mn));
@@ -1516,14 +1521,15 @@ static rkl_status pair_product(FfnPairArgs& a, const void* A, const void* A2, bo
   return RKL_OK;
 }
 
+// (x_live: as a_live above)
 static rkl_status skinny_product(const SkinnyPlan& p, const void* x, const void* W1, int64_t R1, const void* W2, int64_t T,
-                                 int64_t K, float* part, bool follows, cudaStream_t s) {
+                                 int64_t K, int64_t x_live, float* part, bool follows, cudaStream_t s) {
   FfnSkinnyArgs a = {};
   a.cols = static_cast<int>((T + 15) / 16 * 16);
   RKL_TRY(operand_map(&a.w1, W1, R1, K, false));
   a.w2 = a.w1;
   if (W2) RKL_TRY(operand_map(&a.w2, W2, R1, K, false));
-  RKL_TRY(make_map(&a.x, x, false, K, T, K * 2, kBK, a.cols));
+  RKL_TRY(make_map(&a.x, x, false, x_live, T, K * 2, kBK, a.cols));
   a.part = part;
   a.per = p.per;
   a.tiles = p.tiles;
@@ -1576,9 +1582,9 @@ static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_
                                  float* saved, uint8_t* ws, int sms, cudaStream_t s) {
   float* part = reinterpret_cast<float*>(ws + p.off_part);
   if (p.skinny) {
-    RKL_TRY(skinny_product(p.up, x, W_gate, F, W_up, T, H, part, false, s));
+    RKL_TRY(skinny_product(p.up, x, W_gate, F, W_up, T, H, H, part, false, s));
     RKL_TRY(join_skinny(p.up, act, part, ws, p.terms > 1 ? ws + p.plane / 2 : nullptr, saved, T, F, p.terms, s));
-    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, p.terms * T, F, part, true, s));
+    RKL_TRY(skinny_product(p.down, ws, W_down, O, nullptr, p.terms * T, F, p.inner, part, true, s));
     return join_skinny(p.down, -1, part, y, nullptr, nullptr, T, O, p.terms, s);
   }
   FfnPairArgs a = {};
@@ -1588,7 +1594,7 @@ static rkl_status ffn_forward_tc(const FfnPlan& p, const void* x, const void* W_
   FfnPairArgs d = {};
   d.follows = true;
   RKL_TRY(pair_product(d, ws, nullptr, false, W_down, nullptr, false, p.parts > 1 ? static_cast<void*>(part) : y, T, O, F,
-                       false, p.parts, p.parts > 1 ? p.part_rows : 0));
+                       false, p.inner, p.parts, p.parts > 1 ? p.part_rows : 0));
   RKL_CUDA(launch_ffn_pair(FFN_GEMM, act, d, sms, s));
   return p.parts > 1 ? join_pair(p, part, y, T, O, s) : RKL_OK;
 }
@@ -1619,7 +1625,7 @@ static rkl_status ffn_backward_tc(const FfnPlan& p, const void* x, const void* W
   const bool joined = p.parts > 1 || p.terms > 1;
   if (dx)
     RKL_TRY(pair_product(d, dg, du, false, W_gate, W_up, true, joined ? static_cast<void*>(part) : dx, rows, H, F, false,
-                         p.parts, joined ? p.part_rows : 0));
+                         p.inner, p.parts, joined ? p.part_rows : 0));
   if (dW_gate) RKL_TRY(pair_product(d, dg, nullptr, true, x, nullptr, true, dW_gate, F, H, rows, false));
   if (dW_up) RKL_TRY(pair_product(d, du, nullptr, true, x, nullptr, true, dW_up, F, H, rows, false));
   if (dW_down) RKL_TRY(pair_product(d, dy, nullptr, true, a_plane, nullptr, true, dW_down, O, F, rows, false));
