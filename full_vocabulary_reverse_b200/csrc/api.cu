@@ -1444,7 +1444,7 @@ static FfnPlan ffn_plan(rkl_dtype dtype, int64_t T, int64_t H, int64_t F, int64_
     p.total = p.off_pad + (backward ? p.terms * (x + y) + x + 2 * (2 * wide + down) : x + 2 * wide + down + y);
     return p;
   }
-  if (p.tc && T <= kFfnTermRows && (T * F <= kFfnTermElements || T * (H < O ? H : O) <= kFfnTermResults)) p.terms = 2;
+  if (p.tc && T <= kFfnTermRows && (T * F <= kFfnTermElements || T * (backward ? H : O) <= kFfnTermResults)) p.terms = 2;
   p.inner = F;
   p.plane = size_t(T) * F * (dtype == RKL_BF16 ? 2 * p.terms : 4);
   p.off_counter = align256((backward ? 3 : 1) * p.plane);

@@ -363,14 +363,17 @@ constexpr int kFfnSkinnyRows = 128;  // rows up to which the weights are the M o
 // Where few numbers make up the result, a, dg and du are held in two bf16 terms,
 // the second under the first as so many rows more.  Many operands' roundings
 // average: they leave a result's error (2-norm) at 1.4 times that of its own
-// rounding.  Of few, heavy-tailed ones, one large a decides: 1.6 times at T = 2,
-// F = 112; with two terms 1.0.  Up to 4096 elements of a, or 1024 of y or dx, the
-// passes are bound by their launches and two terms add 1 us to a forward pass
-// (11.7 -> 12.9) and 11 to a backward pass (22.7 -> 33.8); everywhere up to 64 rows
-// they would cost 10 percent of 1 row at H = 2048, F = 6144 and 28 of 64 rows at
-// H = 1160, F = 2712.
+// rounding.  Of few, heavy-tailed ones one large a decides, and few results have no
+// average: of 12 draws the worst was 1.8 at T = 2, F = 112; with F = 8192, 3.3 for
+// 32 results, 1.7 for 256, 1.5 from 1024 to 4096.  With two terms all are 1.0.  A
+// pass goes by the results that it has: T O of y, T H of dx (the gradients of the
+// weights have many).  Two terms take 1 to 4 us of a forward pass (T = 2, H = 856, F
+// = 112: 10.9 -> 11.4; T = 1, H = O = 1536, F = 8192: 18.8 -> 20.9; F = 65536: 102 ->
+// 104) and 8 to 11 of a backward pass (21 -> 32, 74 -> 82; F = 65536: 362 -> 388).
+// Everywhere up to 64 rows they would cost 10 percent of 1 row at H = 2048, F = 6144
+// and 28 of 64 rows at H = 1160, F = 2712.
 constexpr int kFfnTermRows = 64;  // at most: two terms of them are one K step
-constexpr long long kFfnTermElements = 4096, kFfnTermResults = 1024;
+constexpr long long kFfnTermElements = 4096, kFfnTermResults = 1536;
 struct FfnPairProduct {
   CUtensorMap a[2], b[2];  // bf16, box {64, 128} K-major or {64, 64} MN-major; FFN_UP: b = Wg, Wu
   CUtensorMap c;           // bf16 result, box {32, 32}, 64-byte swizzle; part_rows > 0: fp32 [parts * part_rows, N], box {32, 32}

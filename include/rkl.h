@@ -435,10 +435,11 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
  *
  * Products accumulate in fp32; g, u, act and its derivative are fp32.  a, and
  * in the backward pass a, dg and du, are rounded once to dtype as operands of
- * the next product; in bf16 with up to 64 rows, and T F <= 4096 or T H or T O <=
- * 1024 (widths rounded up to 8), they are held in two bf16 terms instead (2^-16
- * relative): so few elements do not average their roundings.  (A product with an
- * infinite weight, row or gradient may then be NaN instead of infinite.)
+ * the next product; in bf16 with up to 64 rows, and T F <= 4096 or T O (in the
+ * backward pass T H) <= 1536 (widths rounded up to 8), they are held in two bf16
+ * terms instead (2^-16 relative): so few elements do not average their roundings.
+ * (A product with an infinite weight, row or gradient may then be NaN instead of
+ * infinite.)
  *
  * saved: g and u for the backward pass, fp32, rkl_ffn_saved_size elements in an
  * order of the library's own (NULL in the forward pass alone: not stored).  The

@@ -1,5 +1,5 @@
 """The gated feed-forward block beyond the ordinary call: infinite rows at odd
-widths."""
+widths, and how many bf16 terms its operands have."""
 
 import pytest
 import torch
@@ -31,3 +31,20 @@ def test_infinite_rows_at_odd_widths(T, H, F, O):
         assert dx[T // 2].isinf().all() and dx[others].isfinite().all()
         if T > 64:  # (in two terms, which few rows may take, a weight's gradient may be infinity - infinity)
             assert all(w.isinf().all() for w in (dwg, dwu, dwd))
+
+
+@pytest.mark.parametrize("T,F,N", [(5, 2048, 1024), (9, 1000, 256), (64, 128, 1032)])
+def test_a_width_beside_the_result_does_not_change_its_digits(T, F, N):
+    """y [T, N] does not know how wide x is, nor dx [T, N] how wide dy: a's, dg's and du's terms go by the results."""
+    gen = torch.Generator().manual_seed(F)
+    r = lambda *s: torch.randn(s, generator=gen).bfloat16().cuda()  # noqa: E731
+    wide = lambda t: torch.cat([t, torch.zeros(t.shape[0], 248 - t.shape[1], dtype=t.dtype, device="cuda")], 1)  # noqa: E731
+    x, wg, wu, wd = r(T, 8), r(F, 8), r(F, 8), r(N, F)
+    y = ffn_forward(x, wg, wu, wd)[0]
+    # zeros beside x and the weights add nothing to g and u
+    assert torch.equal(y, ffn_forward(wide(x), wide(wg), wide(wu), wd)[0])
+    x, wg, wu, wd, dy = r(T, N), r(F, N), r(F, N), r(8, F), r(T, 8)
+    saved = ffn_forward(x, wg, wu, wd, save=True)[1]
+    dx = ffn_backward(x, wg, wu, wd, dy, saved)[0]
+    tall = wide(wd.t().contiguous()).t().contiguous()
+    assert torch.equal(dx, ffn_backward(x, wg, wu, tall, wide(dy), saved)[0])
