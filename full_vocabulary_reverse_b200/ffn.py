@@ -2,8 +2,9 @@
 
     y = (act(x W_gate^T) * (x W_up^T)) W_down^T
 
-``gated_ffn`` is differentiable; ``ffn_forward`` and ``ffn_backward`` are the
-single passes.  Everything runs in the CUDA library on the current stream."""
+``gated_ffn`` is differentiable (in reverse mode); ``ffn_forward`` and
+``ffn_backward`` are the single passes, outside autograd.  Everything runs in
+the CUDA library on the current stream."""
 
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import ctypes
 from functools import lru_cache
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from .binding import DT_BF16, DT_FP32, RKLError, _check, _on_device, _raw_stream, lib
@@ -109,7 +111,7 @@ def ffn_backward(x, W_gate, W_up, W_down, dy, saved, activation=ACT_SILU, needs=
 class _GatedFFN(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W_gate, W_up, W_down, activation):
-        y, saved = ffn_forward(x, W_gate, W_up, W_down, activation, save=True)
+        y, saved = ffn_forward(x, W_gate, W_up, W_down, activation, save=any(ctx.needs_input_grad))
         ctx.save_for_backward(x, W_gate, W_up, W_down, saved)
         ctx.activation = activation
         return y
@@ -117,14 +119,17 @@ class _GatedFFN(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
+        if forward_ad._current_level >= 0 and forward_ad.unpack_dual(dy).tangent is not None:
+            raise NotImplementedError("gated_ffn has no jvp: no forward mode through its backward pass")
         x, W_gate, W_up, W_down, saved = ctx.saved_tensors
         return ffn_backward(x, W_gate, W_up, W_down, dy, saved, ctx.activation, ctx.needs_input_grad[:4]) + (None,)
 
 
 def gated_ffn(x, W_gate, W_up, W_down, activation=ACT_SILU):
     """y = (act(x W_gate^T) * (x W_up^T)) W_down^T for x [..., H], W_gate and
-    W_up [F, H], W_down [O, F]; differentiable in all four.  Keeps g and u (fp32)
-    for the backward pass only where a gradient is wanted.
+    W_up [F, H], W_down [O, F]; differentiable in all four, in reverse mode (a
+    tangent of forward mode is refused).  Keeps g and u (fp32) for the backward
+    pass only where a gradient is wanted.
 
     To capture a backward pass in a CUDA graph, let no autograd graph of the
     same leaves from another stream be alive (PyTorch would tie the capture to
@@ -134,7 +139,9 @@ def gated_ffn(x, W_gate, W_up, W_down, activation=ACT_SILU):
     if x.dim() < 1:
         raise RKLError(2, "x [..., H] expected")
     rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (x, W_gate, W_up, W_down)):
+    # (inside a forward-mode level autograd looks for tangents and refuses them)
+    if forward_ad._current_level >= 0 or \
+            torch.is_grad_enabled() and any(t.requires_grad for t in (x, W_gate, W_up, W_down)):
         y = _GatedFFN.apply(rows, W_gate, W_up, W_down, activation)
     else:
         y = ffn_forward(rows, W_gate, W_up, W_down, activation)[0]

@@ -1,10 +1,11 @@
 """The gated feed-forward block beyond the ordinary call: infinite rows at odd
-widths, and how many bf16 terms its operands have."""
+widths, how many bf16 terms its operands have, forward mode (which it has not)."""
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
-from full_vocabulary_reverse_b200 import ACT_RELU, ffn_backward, ffn_forward
+from full_vocabulary_reverse_b200 import ACT_RELU, ffn_backward, ffn_forward, gated_ffn
 from full_vocabulary_reverse_b200 import binding as rb
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,40 @@ def test_a_width_beside_the_result_does_not_change_its_digits(T, F, N):
     dx = ffn_backward(x, wg, wu, wd, dy, saved)[0]
     tall = wide(wd.t().contiguous()).t().contiguous()
     assert torch.equal(dx, ffn_backward(x, wg, wu, tall, wide(dy), saved)[0])
+
+
+def block(T=4, H=16, F=32, O=8):
+    gen = torch.Generator().manual_seed(0)
+    return [torch.randn(s, generator=gen).bfloat16().cuda() for s in ((T, H), (F, H), (F, H), (O, F))]
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_is_refused(which, grad):
+    ins = block()
+    with fwd.dual_level(), torch.set_grad_enabled(grad):
+        ins[which] = fwd.make_dual(ins[which], torch.ones_like(ins[which]))
+        with pytest.raises(NotImplementedError, match="jvp"):
+            gated_ffn(*ins)
+
+
+def test_forward_mode_over_the_backward_pass_is_refused():
+    ins = [t.requires_grad_(True) for t in block()]
+    y = gated_ffn(*ins)
+    with fwd.dual_level():
+        dy = fwd.make_dual(torch.ones_like(y), torch.ones_like(y))
+        with pytest.raises(NotImplementedError, match="jvp"):
+            torch.autograd.grad(y, ins, dy)
+
+
+def test_a_level_without_tangents_changes_nothing():
+    ins = block()
+    y = gated_ffn(*ins)
+    with fwd.dual_level():
+        assert torch.equal(gated_ffn(*ins), y)
+        ins[0].requires_grad_(True)
+        z = gated_ffn(*ins)
+        assert torch.equal(z, y)
+        a, = torch.autograd.grad(z, [ins[0]], torch.ones_like(z))
+    b, = torch.autograd.grad(gated_ffn(*ins), [ins[0]], torch.ones_like(y))
+    assert torch.equal(a, b)
