@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 #include <cmath>
@@ -100,22 +101,48 @@ LaunchScope::~LaunchScope() {
 
 // ------------------------------------------------------------------ devices
 struct DevState {
-  bool ready = false;
   int sms = 0;
+  std::vector<unsigned long long> ready;  // contexts that the kernels' attributes are set in
 };
 static std::mutex g_dev_mu;
 static DevState g_devs[64];
 
+// A function of the driver by its name; nullptr where there is none.
+static void* driver_entry(const char* name) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  const bool found = cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) == cudaSuccess;
+  return found && q == cudaDriverEntryPointSuccess ? p : nullptr;
+}
+
+// The current context's number.  A thread that has made no runtime call yet
+// (autograd's backward thread) has no current context, which encoding a tensor
+// map needs: it gets the device's own.  Another one that the caller has made
+// current stays so.
+static cudaError_t need_context(int dev, unsigned long long* id) {
+  typedef CUresult (*GetCurrentFn)(CUcontext*);
+  typedef CUresult (*GetIdFn)(CUcontext, unsigned long long*);
+  static const GetCurrentFn get = reinterpret_cast<GetCurrentFn>(driver_entry("cuCtxGetCurrent"));
+  static const GetIdFn number = reinterpret_cast<GetIdFn>(driver_entry("cuCtxGetId"));
+  if (get == nullptr || number == nullptr) return cudaErrorNotSupported;
+  CUcontext current = nullptr;
+  if (get(&current) != CUDA_SUCCESS || current == nullptr) {
+    const cudaError_t e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (get(&current) != CUDA_SUCCESS) return cudaErrorDeviceUninitialized;
+  }
+  return number(current, id) == CUDA_SUCCESS ? cudaSuccess : cudaErrorDeviceUninitialized;
+}
+
 static rkl_status device_setup(int* sms) {
   int dev = 0;
+  unsigned long long context = 0;
   RKL_CUDA(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(RKL_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
-  // A thread that has made no runtime call yet (autograd's backward thread)
-  // has no current context, which encoding a tensor map needs.
-  RKL_CUDA(cudaSetDevice(dev));
+  RKL_CUDA(need_context(dev, &context));
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DevState& d = g_devs[dev];
-  if (!d.ready) {
+  if (std::find(d.ready.begin(), d.ready.end(), context) == d.ready.end()) {
     int major = 0, minor = 0;
     RKL_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
     RKL_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
@@ -125,7 +152,7 @@ static rkl_status device_setup(int* sms) {
     RKL_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
     RKL_CUDA(tc_setup(dev));
     RKL_CUDA(ffn_tc_setup());
-    d.ready = true;
+    d.ready.push_back(context);
   }
   *sms = d.sms;
   return RKL_OK;
@@ -137,15 +164,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 static EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
+  static const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(driver_entry("cuTensorMapEncodeTiled"));
   return fn;
 }
 
