@@ -58,7 +58,8 @@ __device__ __forceinline__ float act_with_slope(float g, float* slope) {
   }
   if (ACT == ACT_GELU_TANH) {
     // g (1 + tanh(w)) / 2 = g sigmoid(2 w), w = sqrt(2 / pi) (g + 0.044715 g^3)
-    const float q = g * g;
+    // (far out s is 0 or 1 and s (1 - s) 0; a finite g^2 keeps 0 x infinity out of the slope)
+    const float q = fminf(g * g, 1e12f);
     const float s = act_sigmoid<FAST>(1.5957691216057308f * g * fmaf(0.044715f, q, 1.f));
     *slope = fmaf(s * (1.f - s) * g, 1.5957691216057308f * fmaf(0.134145f, q, 1.f), s);
     return g * s;

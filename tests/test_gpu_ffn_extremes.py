@@ -1,11 +1,13 @@
 """The gated feed-forward block beyond the ordinary call: infinite rows at odd
-widths, how many bf16 terms its operands have, forward mode (which it has not)."""
+widths, how many bf16 terms its operands have, forward mode (which it has not),
+gates far out."""
 
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
 
-from full_vocabulary_reverse_b200 import ACT_RELU, ffn_backward, ffn_forward, gated_ffn
+from full_vocabulary_reverse_b200 import (ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SILU, ffn_backward, ffn_forward,
+                                          gated_ffn)
 from full_vocabulary_reverse_b200 import binding as rb
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +88,20 @@ def test_a_level_without_tangents_changes_nothing():
         a, = torch.autograd.grad(z, [ins[0]], torch.ones_like(z))
     b, = torch.autograd.grad(gated_ffn(*ins), [ins[0]], torch.ones_like(y))
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", [ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU])
+@pytest.mark.parametrize("T", [1, 300])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_gates_whose_square_leaves_fp32(sign, T, kind, dtype):
+    """g = +-2^67 and u = 1, powers of two throughout: act' is 1 or 0, and nothing is NaN."""
+    full = lambda shape, v: torch.full(shape, v, dtype=dtype, device="cuda")  # noqa: E731
+    x, wg, wu, wd = full((T, 8), 2.0 ** 31), full((8, 8), sign * 2.0 ** 33), full((8, 8), 2.0 ** -34), full((8, 8), 1.0)
+    dy = full((T, 8), 2.0 ** -3)
+    y, saved = ffn_forward(x, wg, wu, wd, kind, save=True)
+    dx, dwg, dwu, dwd = ffn_backward(x, wg, wu, wd, dy, saved, kind)
+    on = 1.0 if sign > 0 else 0.0
+    # a = g u = 2^67; da = 8 x 2^-3 = 1, dg = 1, du = 2^67; dx = 8 (2^33 + 2^67 2^-34), the weights over T rows
+    for got, want in ((y, 2.0 ** 70), (dx, 2.0 ** 37), (dwg, T * 2.0 ** 31), (dwu, T * 2.0 ** 98), (dwd, T * 2.0 ** 64)):
+        assert torch.equal(got, torch.full_like(got, on * want)), (got.flatten()[0], want)
