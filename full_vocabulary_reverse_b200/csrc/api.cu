@@ -102,7 +102,8 @@ LaunchScope::~LaunchScope() {
 // ------------------------------------------------------------------ devices
 struct DevState {
   int sms = 0;
-  std::vector<unsigned long long> ready;  // contexts that the kernels' attributes are set in
+  unsigned long long ready[8] = {};  // the last contexts that the kernels' attributes were set in
+  int next = 0;
 };
 static std::mutex g_dev_mu;
 static DevState g_devs[64];
@@ -142,17 +143,20 @@ static rkl_status device_setup(int* sms) {
   RKL_CUDA(need_context(dev, &context));
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DevState& d = g_devs[dev];
-  if (std::find(d.ready.begin(), d.ready.end(), context) == d.ready.end()) {
+  if (d.sms == 0 || std::find(d.ready, d.ready + 8, context) == d.ready + 8) {
     int major = 0, minor = 0;
     RKL_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
     RKL_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
     if (major != 10 || minor != 0)
       return fail(RKL_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a (B200)", dev, major,
                   minor);
-    RKL_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
+    int count = 0;
+    RKL_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev));
     RKL_CUDA(tc_setup(dev));
     RKL_CUDA(ffn_tc_setup());
-    d.ready.push_back(context);
+    d.sms = count;
+    d.ready[d.next] = context;
+    d.next = (d.next + 1) % 8;
   }
   *sms = d.sms;
   return RKL_OK;

@@ -4,6 +4,8 @@
     opt = AdamW([W_gate, W_up, W_down, W_s], lr=1e-4, weight_decay=[0.1] * 4, state_bits=8)
     loss.backward()
     norm = opt.step(max_norm=1.0)
+    for w in opt.params:
+        w.grad = None  # backward passes add to .grad; a step leaves it
 
 A step is one launch (two more with ``max_norm``), with nothing copied to the
 device and no host synchronisation: it can be captured in a CUDA graph, whose
@@ -88,7 +90,8 @@ def _dtype_codes(tensors, what):
 
 def grad_norm(grads):
     """The 2-norm of all gradients together, a 1-element fp32 tensor on their
-    device (no host synchronisation).  ``None`` entries are passed over."""
+    device (no host synchronisation), outside autograd.  ``None`` entries are
+    passed over."""
     grads = [g for g in grads if g is not None]
     if not grads:
         raise RKLError(2, "grad_norm needs a gradient")
@@ -117,7 +120,9 @@ class AdamW:
     codes with an fp32 scale for 256 elements).  ``master_weights``: keep fp32
     copies of the parameters and update those; the parameters are their
     rounded values (without it a bf16 parameter loses updates below half its
-    last place).  ``seed``: of the 8-bit form's stochastic rounding.
+    last place).  ``seed``: of the 8-bit form's stochastic rounding.  To follow a
+    schedule, give ``step`` its ``lr`` (or change the number in the tensor); there
+    are no parameter groups, and gradients are cleared by the caller.
 
     The state: ``exp_avg``, ``exp_avg_sq`` (flat; tensor i at
     ``[offsets[i], offsets[i] + numel)``), for 8 bits ``exp_avg_scale`` and
