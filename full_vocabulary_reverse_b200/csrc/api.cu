@@ -102,7 +102,7 @@ LaunchScope::~LaunchScope() {
 // ------------------------------------------------------------------ devices
 struct DevState {
   int sms = 0;
-  unsigned long long ready[8] = {};  // the last contexts that the kernels' attributes were set in
+  unsigned long long ready[8] = {};  // the last contexts that the kernels' attributes were set in (0: none)
   int next = 0;
 };
 static std::mutex g_dev_mu;
@@ -132,7 +132,9 @@ static cudaError_t need_context(int dev, unsigned long long* id) {
     if (e != cudaSuccess) return e;
     if (get(&current) != CUDA_SUCCESS) return cudaErrorDeviceUninitialized;
   }
-  return number(current, id) == CUDA_SUCCESS ? cudaSuccess : cudaErrorDeviceUninitialized;
+  if (number(current, id) != CUDA_SUCCESS) return cudaErrorDeviceUninitialized;
+  ++*id;  // (above 0)
+  return cudaSuccess;
 }
 
 static rkl_status device_setup(int* sms) {
@@ -143,7 +145,7 @@ static rkl_status device_setup(int* sms) {
   RKL_CUDA(need_context(dev, &context));
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DevState& d = g_devs[dev];
-  if (d.sms == 0 || std::find(d.ready, d.ready + 8, context) == d.ready + 8) {
+  if (std::find(d.ready, d.ready + 8, context) == d.ready + 8) {
     int major = 0, minor = 0;
     RKL_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
     RKL_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));

@@ -13,7 +13,8 @@
 //          and u in fp32 where a backward pass wants them
 //   DGATE  da from the accumulator, g and u from memory: a, dg and du, each
 //          rounded once as the next products' operands (DGATE_TERMS, for few
-//          elements: in two bf16 terms, the second as T rows more)
+//          elements: in two bf16 terms, the second as T rows more; its up to 92
+//          bytes of spills at 168 registers do not show beside the launches)
 //   GEMM   a list of up to four products in one launch (the backward pass runs
 //          dx, dWg, dWu and dWd together, so that one's tail is filled by
 //          another's tiles), bf16 results, or fp32 parts of a split K

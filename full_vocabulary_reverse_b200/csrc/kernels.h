@@ -369,9 +369,9 @@ constexpr int kFfnSkinnyRows = 128;  // rows up to which the weights are the M o
 // pass goes by the results that it has: T O of y, T H of dx (the gradients of the
 // weights have many).  Two terms take 1 to 4 us of a forward pass (T = 2, H = 856, F
 // = 112: 10.9 -> 11.4; T = 1, H = O = 1536, F = 8192: 18.8 -> 20.9; F = 65536: 102 ->
-// 104) and 8 to 11 of a backward pass (21 -> 32, 74 -> 82; F = 65536: 362 -> 388).
-// Everywhere up to 64 rows they would cost 10 percent of 1 row at H = 2048, F = 6144
-// and 28 of 64 rows at H = 1160, F = 2712.
+// 104), 7 to 11 of a backward pass (21 -> 32, 74 -> 82) and more of a wide one (F =
+// 65536: 362 -> 388).  Everywhere up to 64 rows they would cost 10 percent of 1 row
+// at H = 2048, F = 6144 and 28 of 64 rows at H = 1160, F = 2712.
 constexpr int kFfnTermRows = 64;  // at most: two terms of them are one K step
 constexpr long long kFfnTermElements = 4096, kFfnTermResults = 1536;
 struct FfnPairProduct {

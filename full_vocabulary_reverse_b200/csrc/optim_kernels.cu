@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constan
 // on changing gradients, about 15 where the gradient stays the same and moments
 // stop next to borders).
 // Paired fp32 instructions took 10 % of the instructions away; 24 warps an SM
-// with the next block's lines on their way to L2 ran faster than 16 or 32.
+// with the next block's lines on their way to L2 ran faster than 16 or 32 (80
+// registers a thread; the second look spills 20 bytes).
 //
 // Beside the codes, fp32 arithmetic finds the values that lie within its error
 // of a border between two codes; their block then looks at those again in 64
