@@ -450,6 +450,7 @@ rkl_status rkl_forward_hidden_noalloc(const void* h_s, const void* h_t,
  *     dW_down = dy^T a
  *
  * Each of its outputs (of dtype) may be NULL: it is left out.  relu'(0) = 0.
+ * No output may overlap an input, another output or the workspace.
  * The workspace (16-byte aligned) is free again when the call's work is done. */
 typedef enum rkl_activation {
   RKL_ACT_SILU = 0,      /* g / (1 + e^-g) */

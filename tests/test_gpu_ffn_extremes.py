@@ -1,6 +1,6 @@
 """The gated feed-forward block beyond the ordinary call: infinite rows at odd
 widths, how many bf16 terms its operands have, forward mode (which it has not),
-gates far out."""
+gates far out, offsets past 32 bits, two streams at once."""
 
 import pytest
 import torch
@@ -9,6 +9,7 @@ import torch.autograd.forward_ad as fwd
 from full_vocabulary_reverse_b200 import (ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SILU, ffn_backward, ffn_forward,
                                           gated_ffn)
 from full_vocabulary_reverse_b200 import binding as rb
+from tests import ffn_reference as R
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,44 @@ def test_gates_whose_square_leaves_fp32(sign, T, kind, dtype):
     # a = g u = 2^67; da = 8 x 2^-3 = 1, dg = 1, du = 2^67; dx = 8 (2^33 + 2^67 2^-34), the weights over T rows
     for got, want in ((y, 2.0 ** 70), (dx, 2.0 ** 37), (dwg, T * 2.0 ** 31), (dwu, T * 2.0 ** 98), (dwd, T * 2.0 ** 64)):
         assert torch.equal(got, torch.full_like(got, on * want)), (got.flatten()[0], want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,F,O", [(270003, 8, 8192, 8), (270003, 9, 8193, 7)])
+def test_offsets_past_32_bits(T, H, F, O, dtype):
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB of free memory")
+    gen = torch.Generator("cuda").manual_seed(1)
+    r = lambda rows, cols, s: (torch.randn((rows, cols), generator=gen, device="cuda") * s).to(dtype)  # noqa: E731
+    x, wg, wu, wd, dy = r(T, H, 1), r(F, H, H ** -0.5), r(F, H, H ** -0.5), r(O, F, F ** -0.5), r(T, O, 0.1)
+    n = 700
+    dy[:-n] = 0  # the other rows add exact zeros to the weights' gradients
+    y, saved = ffn_forward(x, wg, wu, wd, save=True)
+    grads = ffn_backward(x, wg, wu, wd, dy, saved)
+    assert rb.device_error() == 0 and saved.numel() > 1 << 32
+    R.check([y[-n:], grads[0][-n:], *grads[1:]], R.block(x[-n:], wg, wu, wd, R.SILU, dy[-n:]), dtype)
+    R.check([y[:n]], R.block(x[:n], wg, wu, wd, R.SILU), dtype)
+    assert not grads[0][:-n].any()
+
+
+def test_two_streams_at_once():
+    gen = torch.Generator().manual_seed(1)
+    r = lambda *s: (torch.randn(s, generator=gen) * s[-1] ** -0.5).bfloat16().cuda()  # noqa: E731
+    blocks = [[r(T, 512), r(1024, 512), r(1024, 512), r(512, 1024)] for T in (3, 700)]
+    want = [ffn_forward(*b)[0] for b in blocks]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(50):
+        for b, s, g in zip(blocks, streams, got):
+            with torch.cuda.stream(s):
+                g.append(ffn_forward(*b)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for w, g in zip(want, got) for y in g) and rb.device_error() == 0
+
+
+def test_one_row_without_a_batch_and_no_batch():
+    x, wg, wu, wd = block()
+    y = gated_ffn(x[0], wg, wu, wd)
+    assert y.shape == (8,) and torch.equal(y, gated_ffn(x[:1], wg, wu, wd)[0])
+    assert gated_ffn(x.new_empty(0, 5, 16), wg, wu, wd).shape == (0, 5, 8)
